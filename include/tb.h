@@ -70,12 +70,14 @@ typedef enum {
 #define TB_FLAG_TIMEOUT     0x2u  /* a bounded wait gave up; the output is invalid */
 #define TB_FLAG_IDX_OVERFLOW 0x4u /* selected set larger than idx_cap: truncated */
 #define TB_FLAG_BAD_CACHE   0x8u  /* tb_kv_append: a cache address was null or misaligned: skipped */
+#define TB_FLAG_BAD_PATH    0x10u /* tb_tree_accept: a path that does not rise or leaves the drafted rows: skipped */
 
 /* Shapes shared by the cache-facing calls. */
 typedef struct {
     int32_t batch;       /* sequences, <= 65535 */
     int32_t n_q_heads;   /* Hq  */
-    int32_t n_kv_heads;  /* Hkv <= 65535; Hq / Hkv must be 4 */
+    int32_t n_kv_heads;  /* Hkv <= 65535; Hq / Hkv must be 4 (1, 2, 4, 8 or 16 for the
+                          * calls that take several new tokens per sequence) */
     int32_t head_dim;    /* d:  64 or 128 */
     int32_t d_proj;      /* d': 16 or 32 */
     int32_t ctx_cap;     /* rows per (sequence, KV head) in K, V and K' */
@@ -480,6 +482,109 @@ tb_status tb_sparse_decode_attn_noalloc(const tb_dims *dims, const tb_bf16 *Q, c
                                         const tb_bf16 *V, const int32_t *ctx_len, int32_t sink,
                                         int32_t window, const uint32_t *sel_bits, float scale,
                                         float *out, void *stream);
+
+/* ---- several new tokens per sequence --------------------------------------- */
+/* The calls below handle several tokens of a sequence at once: a prompt (or a
+ * chunk of one) on its way into the cache, and a tree of drafted tokens that
+ * is verified in one step.  No counterpart on the pages, which start from a
+ * filled cache and decode one token at a time; these calls fill the cache and
+ * let the decode loop continue behind it.
+ *
+ * Tokens are packed: sequence b's are tokens q_begin[b] .. q_begin[b+1] of
+ * the packed arrays (q_begin: [batch + 1] int32, device, rising from 0; a
+ * sequence may have none), n_tokens (host) is the packed arrays' token count;
+ * tokens at or past q_begin[batch] are neither read nor written.  n =
+ * q_begin[b+1] - q_begin[b] and T = ctx_len[b], which counts the new tokens:
+ * token i of sequence b sits at cache row T - n + i.  A sequence with n = 0
+ * is not looked at (its ctx_len may be 0).  These calls take groups of 1, 2,
+ * 4, 8 or 16 query heads per KV head (the other calls need 4), head_dim 64 or
+ * 128, and ignore d_proj. */
+
+/* Norms of queries and keys, position rotation and cache write in one pass.
+ * For every token and every query and key head row x (head_dim values):
+ *
+ *   y = x * weight / sqrt(mean(x^2) + eps)       (no weight: y = x)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin),  angle = position * inv_freq[j]
+ *
+ * for the rot_dim / 2 pairs j of the first rot_dim values: (a, b) = (j, j +
+ * rot_dim / 2) for TB_ROPE_HALF, (2j, 2j + 1) for TB_ROPE_INTERLEAVED.  The
+ * angle is a product in fp64, the rest fp32, one rounding to bf16 at the end.
+ *
+ *   qkv       [n_tokens] rows of row_stride elements (a multiple of 8, >= (Hq +
+ *             2 Hkv) * d), each Hq query heads, Hkv key heads, Hkv value heads
+ *   pos       [n_tokens] int32 positions, or NULL: the token's cache row.  (A
+ *             drafted token's position is its depth in the tree, not its row.)
+ *   q_weight, k_weight  [d] bf16, either may be NULL: that norm is left out
+ *   inv_freq  [rot_dim / 2] double (device, 8-byte aligned), radians per
+ *             position; rot_dim a multiple of 8 in [0, d] (0: no rotation)
+ *   Q         [n_tokens][Hq][d] bf16 out; must not overlap qkv
+ *   K, V      the caches: row T - n + i of every KV head written
+ * A token whose cache row lies outside [0, ctx_cap) gets its Q row only, and
+ * TB_FLAG_CTX_RANGE is raised in ws (>= 256 bytes). */
+#define TB_ROPE_HALF 0
+#define TB_ROPE_INTERLEAVED 1
+tb_status tb_norm_rope_append(const tb_dims *dims, const tb_bf16 *qkv, int64_t row_stride, const int32_t *q_begin,
+                              int32_t n_tokens, const int32_t *ctx_len, const int32_t *pos, const tb_bf16 *q_weight,
+                              const tb_bf16 *k_weight, float eps, const double *inv_freq, int32_t rot_dim,
+                              int32_t style, tb_bf16 *Q, tb_bf16 *K, tb_bf16 *V, void *ws, size_t ws_bytes,
+                              void *stream);
+
+/* Causal attention of packed prompts over the cache (which holds the new
+ * tokens' rows already).  For token i of sequence b and query head h of KV
+ * head g:
+ *
+ *   out = sum_t softmax_t( scale * Q[b,i,h].K[b][g][t] ) V[b][g][t],   t <= T - n + i
+ *
+ *   Q, out    [n_tokens][Hq][d] bf16; out must not overlap Q, K or V
+ *   max_new   host: an upper bound on every sequence's n (sizes the grid); a
+ *             longer sequence raises TB_FLAG_CTX_RANGE and its tokens past
+ *             max_new are left out
+ *   scale     finite, > 0
+ * With T = n this is a whole prompt; with T > n, a chunk behind cached rows;
+ * with n = 1 the decode step.  fp32 logits, softmax statistics and sums; the
+ * weights are rounded to bf16 for the product with V, the result to bf16.
+ * Cache rows at or past T cannot reach the result, whatever they hold.  A
+ * ctx_len outside [1, ctx_cap] is clamped and one smaller than n leaves the
+ * first tokens without a row (their result is 0); both raise
+ * TB_FLAG_CTX_RANGE.  batch * Hkv * ctx_cap <= 2^31 - 256.
+ * Tensor cores (tcgen05) with TMA-loaded operands; deterministic. */
+size_t    tb_prompt_attn_workspace_bytes(const tb_dims *dims, int32_t n_tokens, int32_t max_new);
+tb_status tb_prompt_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, const tb_bf16 *V,
+                         const int32_t *q_begin, int32_t n_tokens, int32_t max_new, const int32_t *ctx_len,
+                         float scale, tb_bf16 *out, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention of drafted token trees over the cache: as tb_prompt_attn, but
+ * drafted token i attends to all rows before the drafted ones, t < T - n, and
+ * to the drafted rows t = T - n + j, j < n, whose bit is set:
+ *
+ *   mask      [n_tokens][ceil(max_new / 32)] uint32: bit j % 32 of word j / 32
+ *             of token i's row (j counts within the sequence).  For a tree:
+ *             token i itself and its ancestors.  A token that attends to
+ *             nothing gets 0.
+ * max_new <= 1024; the workspace is tb_tree_attn_workspace_bytes'. */
+size_t    tb_tree_attn_workspace_bytes(const tb_dims *dims, int32_t n_tokens, int32_t max_new);
+tb_status tb_tree_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, const tb_bf16 *V,
+                       const int32_t *q_begin, int32_t n_tokens, int32_t max_new, const int32_t *ctx_len,
+                       const uint32_t *mask, float scale, tb_bf16 *out, void *ws, size_t ws_bytes, void *stream);
+
+/* Keep the accepted path of each sequence's drafted tree: in every layer's K
+ * and V cache (addresses in `caches`, as for tb_kv_append), with T, n as
+ * above,
+ *
+ *   row T - n + j <- row T - n + path[b][j],  j < path_len[b];  new_len[b] = T - n + path_len[b]
+ *
+ *   path      [batch][path_cap] int32: drafted tokens (index within the
+ *             sequence), strictly rising; path_cap <= 1024
+ *   path_len  [batch] int32, 0 (nothing accepted) .. n
+ *   new_len   [batch] int32 out; must not overlap ctx_len
+ * Rows behind the new length keep what they held.  A path that does not rise
+ * or leaves [0, n) moves nothing, keeps new_len[b] = T and raises
+ * TB_FLAG_BAD_PATH in ws (>= 256 bytes); so does n outside [0, T] or T above
+ * ctx_cap.  Projected keys (K') are not touched: project only rows below the
+ * accepted length. */
+tb_status tb_tree_accept(const tb_dims *dims, int32_t n_layers, const uint64_t *caches, const int32_t *q_begin,
+                         const int32_t *ctx_len, const int32_t *path, int32_t path_cap, const int32_t *path_len,
+                         int32_t *new_len, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

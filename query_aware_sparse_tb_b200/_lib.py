@@ -18,10 +18,12 @@ LIB_PATH = os.path.join(_PKG, "libtb.so")
 TB_ABI_VERSION = 10
 TB_OK, TB_ERR_INVALID_ARG, TB_ERR_UNSUPPORTED, TB_ERR_CUDA, TB_ERR_WORKSPACE, TB_ERR_DEVICE_FLAG = range(6)
 TB_FLAG_CTX_RANGE, TB_FLAG_TIMEOUT, TB_FLAG_IDX_OVERFLOW, TB_FLAG_BAD_CACHE = 0x1, 0x2, 0x4, 0x8
+TB_FLAG_BAD_PATH = 0x10
 TB_GROUP_REDUCE = {"max": 0, "sum": 1}
 TB_ATTN_WAIT_ALL, TB_ATTN_PREFETCH_KV = 0, 1
 TB_SELECT_AUTO, TB_SELECT_MULTI_KERNEL, TB_SELECT_CLUSTER = 0, 1, 2
 TB_ATTN_PLAN_STRIDE = 65
+TB_ROPE_HALF, TB_ROPE_INTERLEAVED = 0, 1
 
 EXPORTS = [
     "tb_abi_version", "tb_status_str", "tb_last_error",
@@ -34,6 +36,8 @@ EXPORTS = [
     "tb_sparse_decode_attn", "tb_decode_attn", "tb_sparse_decode_attn_noalloc", "tb_kv_append",
     "tb_selftest_bounded_wait", "tb_attn_set_launch_mode", "tb_attn_launch_mode",
     "tb_select_set_algorithm", "tb_select_algorithm", "tb_attn_plan", "tb_sparse_decode_attn_planned",
+    "tb_norm_rope_append", "tb_prompt_attn_workspace_bytes", "tb_prompt_attn", "tb_tree_attn_workspace_bytes",
+    "tb_tree_attn", "tb_tree_accept",
 ]
 
 
@@ -96,6 +100,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "tb_attn_launch_mode": ([], i32),
         "tb_select_set_algorithm": ([i32], ctypes.c_int),
         "tb_select_algorithm": ([], i32),
+        "tb_norm_rope_append": ([D, P, i64, P, i32, P, P, P, P, f32, P, i32, i32, P, P, P, P, sz, P], ctypes.c_int),
+        "tb_prompt_attn_workspace_bytes": ([D, i32, i32], sz),
+        "tb_prompt_attn": ([D, P, P, P, P, i32, i32, P, f32, P, P, sz, P], ctypes.c_int),
+        "tb_tree_attn_workspace_bytes": ([D, i32, i32], sz),
+        "tb_tree_attn": ([D, P, P, P, P, i32, i32, P, P, f32, P, P, sz, P], ctypes.c_int),
+        "tb_tree_accept": ([D, i32, P, P, P, P, i32, P, P, P, sz, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -317,6 +327,119 @@ def kv_append(d: TbDims, n_layers: int, src, caches, ctx_len, ws, stream=None):
     addresses (K of layer l at 2l, V at 2l+1)."""
     _check(load().tb_kv_append(ctypes.byref(d), int(n_layers), _ptr(src), _ptr(caches), _ptr(ctx_len), _ptr(ws),
                                _bytes(ws), _stream(stream)))
+
+
+# The calls that take several new tokens of a sequence at once check what the C
+# side cannot see: types, shapes against dims, and that every tensor is on one
+# device, which is made current for the call (the default stream is that
+# device's current one).
+
+def _tensor(name, t, dtype, shape, device):
+    if not t.is_cuda:
+        raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes device tensors")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TbError(TB_ERR_INVALID_ARG, f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise TbError(TB_ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes contiguous tensors")
+    if t.device != device:
+        raise TbError(TB_ERR_INVALID_ARG, f"{name} is on {t.device}, the workspace on {device}")
+
+
+def _device_of(ws):
+    if not ws.is_cuda:
+        raise TbError(TB_ERR_INVALID_ARG, "ws: libtb takes device tensors")
+    return ws.device
+
+
+_WORDS = (torch.int32, torch.uint32)
+
+
+def _check_multi(d: TbDims, Q, K, V, q_begin, ctx_len, ws):
+    dev = _device_of(ws)
+    bf = torch.bfloat16
+    _tensor("Q", Q, bf, (Q.shape[0], d.n_q_heads, d.head_dim), dev)
+    for name, t in (("K", K), ("V", V)):
+        _tensor(name, t, bf, (d.batch, d.n_kv_heads, d.ctx_cap, d.head_dim), dev)
+    _tensor("q_begin", q_begin, torch.int32, (d.batch + 1,), dev)
+    _tensor("ctx_len", ctx_len, torch.int32, (d.batch,), dev)
+    return dev
+
+
+def norm_rope_append(d: TbDims, qkv, q_begin, ctx_len, pos, q_weight, k_weight, eps: float, inv_freq,
+                     interleaved: bool, Q, K, V, ws, stream=None):
+    """tb_norm_rope_append: qkv [n_tokens][(Hq + 2 Hkv) * d] bf16 (rows may be
+    further apart); pos [n_tokens] int32 or None (the cache row); q_weight and
+    k_weight [d] bf16 or None; inv_freq [rot_dim / 2] float64 or None; writes Q
+    [n_tokens][Hq][d] and the new rows of the caches K and V."""
+    dev = _check_multi(d, Q, K, V, q_begin, ctx_len, ws)
+    n, width = Q.shape[0], (d.n_q_heads + 2 * d.n_kv_heads) * d.head_dim
+    if not qkv.is_cuda or qkv.device != dev or qkv.dtype != torch.bfloat16 or tuple(qkv.shape) != (n, width) or \
+            qkv.stride(1) != 1:
+        raise TbError(TB_ERR_INVALID_ARG, f"qkv: expected bfloat16 [{n}][{width}] on {dev} with contiguous rows")
+    if pos is not None:
+        _tensor("pos", pos, torch.int32, (n,), dev)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _tensor(name, t, torch.bfloat16, (d.head_dim,), dev)
+    rot = 0
+    if inv_freq is not None:
+        _tensor("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
+        rot = 2 * inv_freq.numel()
+    stride = qkv.stride(0) if n > 1 else max(width, qkv.stride(0))
+    with torch.cuda.device(dev):
+        _check(load().tb_norm_rope_append(ctypes.byref(d), qkv.data_ptr(), stride, _ptr(q_begin), n, _ptr(ctx_len),
+                                          _ptr(pos), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), rot,
+                                          TB_ROPE_INTERLEAVED if interleaved else TB_ROPE_HALF, _ptr(Q), _ptr(K),
+                                          _ptr(V), _ptr(ws), _bytes(ws), _stream(stream)))
+
+
+def prompt_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
+    return load().tb_prompt_attn_workspace_bytes(ctypes.byref(d), int(n_tokens), int(max_new))
+
+
+def prompt_attn(d: TbDims, Q, K, V, q_begin, max_new: int, ctx_len, scale: float, out, ws, stream=None):
+    """tb_prompt_attn: causal attention of packed prompts over the caches;
+    Q and out [n_tokens][Hq][d] bf16, q_begin [batch + 1] int32, max_new an
+    upper bound on a sequence's new tokens."""
+    dev = _check_multi(d, Q, K, V, q_begin, ctx_len, ws)
+    _tensor("out", out, torch.bfloat16, Q.shape, dev)
+    with torch.cuda.device(dev):
+        _check(load().tb_prompt_attn(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(q_begin), Q.shape[0],
+                                     int(max_new), _ptr(ctx_len), float(scale), _ptr(out), _ptr(ws), _bytes(ws),
+                                     _stream(stream)))
+
+
+def tree_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
+    return load().tb_tree_attn_workspace_bytes(ctypes.byref(d), int(n_tokens), int(max_new))
+
+
+def tree_attn(d: TbDims, Q, K, V, q_begin, max_new: int, ctx_len, mask, scale: float, out, ws, stream=None):
+    """tb_tree_attn: as prompt_attn, with the drafted tokens' attention bits
+    mask [n_tokens][ceil(max_new / 32)] (int32 or uint32 words)."""
+    dev = _check_multi(d, Q, K, V, q_begin, ctx_len, ws)
+    _tensor("out", out, torch.bfloat16, Q.shape, dev)
+    _tensor("mask", mask, _WORDS, (Q.shape[0], (int(max_new) + 31) // 32), dev)
+    with torch.cuda.device(dev):
+        _check(load().tb_tree_attn(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(q_begin), Q.shape[0],
+                                   int(max_new), _ptr(ctx_len), _ptr(mask), float(scale), _ptr(out), _ptr(ws),
+                                   _bytes(ws), _stream(stream)))
+
+
+def tree_accept(d: TbDims, n_layers: int, caches, q_begin, ctx_len, path, path_len, new_len, ws, stream=None):
+    """tb_tree_accept: caches as for kv_append; path [batch][path_cap] int32,
+    path_len and new_len [batch] int32."""
+    dev = _device_of(ws)
+    _tensor("caches", caches, torch.int64, (2 * int(n_layers),), dev)
+    _tensor("q_begin", q_begin, torch.int32, (d.batch + 1,), dev)
+    _tensor("path", path, torch.int32, (d.batch, path.shape[-1]), dev)
+    for name, t in (("ctx_len", ctx_len), ("path_len", path_len), ("new_len", new_len)):
+        _tensor(name, t, torch.int32, (d.batch,), dev)
+    with torch.cuda.device(dev):
+        _check(load().tb_tree_accept(ctypes.byref(d), int(n_layers), _ptr(caches), _ptr(q_begin), _ptr(ctx_len),
+                                     _ptr(path), path.shape[1], _ptr(path_len), _ptr(new_len), _ptr(ws), _bytes(ws),
+                                     _stream(stream)))
 
 
 def selftest_bounded_wait(ws, budget_cycles: int, stream=None):

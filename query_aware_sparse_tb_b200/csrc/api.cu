@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "multi.h"
 
 namespace tb {
 
@@ -34,6 +35,7 @@ namespace {
 constexpr int kMaxCtxSelect = 1 << 19;
 constexpr int kMaxInclusiveBudget = 8192;
 constexpr int kMaxCtxAttn = 1 << 22;
+constexpr int kMaxTree = 1024;  // drafted tokens of one sequence
 
 tb_status fail(tb_status s, const char *fmt, ...) {
     va_list ap;
@@ -82,6 +84,34 @@ tb_status check_dims(const tb_dims *d, bool need_dproj, const char *fn) {
     if (need_dproj && d->d_proj != 16 && d->d_proj != 32)
         return fail(TB_ERR_UNSUPPORTED, "%s: d_proj %d not built (16, 32)", fn, d->d_proj);
     return TB_OK;
+}
+
+// The dims of the calls that take several new tokens per sequence: as
+// check_dims, with any group of 1, 2, 4, 8 or 16 heads and no d_proj.
+tb_status check_dims_multi(const tb_dims *d, const char *fn) {
+    if (!d) return fail(TB_ERR_INVALID_ARG, "%s: dims is null", fn);
+    if (d->batch < 1 || d->n_q_heads < 1 || d->n_kv_heads < 1 || d->ctx_cap < 1)
+        return fail(TB_ERR_INVALID_ARG, "%s: batch, head counts and ctx_cap must be >= 1", fn);
+    if (d->n_q_heads % d->n_kv_heads != 0)
+        return fail(TB_ERR_INVALID_ARG, "%s: n_q_heads (%d) not a multiple of n_kv_heads (%d)", fn, d->n_q_heads,
+                    d->n_kv_heads);
+    if (d->batch > 65535 || d->n_kv_heads > 65535)
+        return fail(TB_ERR_UNSUPPORTED, "%s: batch (%d) and n_kv_heads (%d) must be <= 65535", fn, d->batch,
+                    d->n_kv_heads);
+    const int G = d->n_q_heads / d->n_kv_heads;
+    if (G > 16 || (G & (G - 1)) != 0)
+        return fail(TB_ERR_UNSUPPORTED, "%s: groups of 1, 2, 4, 8 or 16 query heads are built (got %d)", fn, G);
+    if (d->head_dim != 64 && d->head_dim != 128)
+        return fail(TB_ERR_UNSUPPORTED, "%s: head_dim %d not built (64, 128)", fn, d->head_dim);
+    if (d->ctx_cap > kMaxCtxAttn)
+        return fail(TB_ERR_UNSUPPORTED, "%s: ctx_cap %d above %d", fn, d->ctx_cap, kMaxCtxAttn);
+    return TB_OK;
+}
+
+// Do [a, a + na) and [b, b + nb) share a byte?
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
 }
 
 tb_status check_ws(void *ws, size_t have, size_t need, const char *fn) {
@@ -331,6 +361,123 @@ tb_status tb_score_select_inclusive(const tb_dims *dims, const float *qp, int64_
                                     uint32_t *sel_bits, void *ws, size_t ws_bytes, void *stream) {
     return score_select_impl(__func__, dims, qp, qp_batch_stride, Kp, ctx_len, sink, window, budget, nbr, 2, idx,
                              idx_cap, count, sel_bits, ws, ws_bytes, stream);
+}
+
+tb_status tb_norm_rope_append(const tb_dims *dims, const tb_bf16 *qkv, int64_t row_stride, const int32_t *q_begin,
+                              int32_t n_tokens, const int32_t *ctx_len, const int32_t *pos, const tb_bf16 *q_weight,
+                              const tb_bf16 *k_weight, float eps, const double *inv_freq, int32_t rot_dim,
+                              int32_t style, tb_bf16 *Q, tb_bf16 *K, tb_bf16 *V, void *ws, size_t ws_bytes,
+                              void *stream) {
+    tb_status s;
+    if ((s = check_dims_multi(dims, __func__)) != TB_OK) return s;
+    if (n_tokens < 0) return fail(TB_ERR_INVALID_ARG, "%s: n_tokens < 0", __func__);
+    if (n_tokens == 0) return TB_OK;  // (empty arrays may have no address)
+    TB_CHECK_PTR(qkv); TB_CHECK_PTR4(q_begin); TB_CHECK_PTR4(ctx_len);
+    TB_CHECK_PTR(Q); TB_CHECK_PTR(K); TB_CHECK_PTR(V);
+    if (pos) TB_CHECK_PTR4(pos);
+    if (q_weight) TB_CHECK_PTR(q_weight);
+    if (k_weight) TB_CHECK_PTR(k_weight);
+    const int64_t width = ((int64_t)dims->n_q_heads + 2 * (int64_t)dims->n_kv_heads) * dims->head_dim;
+    if (row_stride < width || row_stride % 8 != 0)
+        return fail(TB_ERR_INVALID_ARG, "%s: row_stride %lld is below (Hq + 2 Hkv) * d = %lld or not a multiple of 8",
+                    __func__, (long long)row_stride, (long long)width);
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(TB_ERR_INVALID_ARG, "%s: eps is negative or not finite", __func__);
+    if (rot_dim < 0 || rot_dim > dims->head_dim || rot_dim % 8 != 0)
+        return fail(TB_ERR_INVALID_ARG, "%s: rot_dim %d is not a multiple of 8 in [0, head_dim]", __func__, rot_dim);
+    if (rot_dim > 0 && (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0))
+        return fail(TB_ERR_INVALID_ARG, "%s: inv_freq is null or not 8-byte aligned", __func__);
+    if (style != TB_ROPE_HALF && style != TB_ROPE_INTERLEAVED)
+        return fail(TB_ERR_INVALID_ARG, "%s: unknown style %d", __func__, style);
+    if ((long long)n_tokens * ((dims->n_q_heads + 2LL * dims->n_kv_heads + 7) / 8) > 0x7fffffffLL)
+        return fail(TB_ERR_UNSUPPORTED, "%s: n_tokens %d times the heads is too large for one call", __func__, n_tokens);
+    if (overlap(Q, (size_t)n_tokens * dims->n_q_heads * dims->head_dim * 2, qkv, (size_t)n_tokens * row_stride * 2))
+        return fail(TB_ERR_INVALID_ARG, "%s: Q overlaps qkv", __func__);
+    if ((s = check_ws(ws, ws_bytes, kWsHeaderBytes, __func__)) != TB_OK) return s;
+    return cuda_status(launch_norm_rope_append(*dims, qkv, row_stride, q_begin, n_tokens, ctx_len, pos, q_weight,
+                                               k_weight, eps, inv_freq, rot_dim, style, Q, K, V, ws,
+                                               (cudaStream_t)stream),
+                       __func__);
+}
+
+static tb_status check_multi_shape(const tb_dims *dims, int32_t n_tokens, int32_t max_new, bool tree, const char *fn) {
+    tb_status s;
+    if ((s = check_dims_multi(dims, fn)) != TB_OK) return s;
+    if (n_tokens < 0 || max_new < 1)
+        return fail(TB_ERR_INVALID_ARG, "%s: need n_tokens >= 0 and max_new >= 1", fn);
+    if (tree && max_new > kMaxTree)
+        return fail(TB_ERR_UNSUPPORTED, "%s: max_new %d above %d drafted tokens", fn, max_new, kMaxTree);
+    if ((long long)dims->batch * dims->n_kv_heads * dims->ctx_cap > 0x7fffff00LL)
+        return fail(TB_ERR_UNSUPPORTED, "%s: more than 2^31 - 256 cache rows", fn);
+    if ((long long)n_tokens * dims->n_q_heads > 0x7fffffffLL)
+        return fail(TB_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query rows", fn);
+    return TB_OK;
+}
+
+size_t tb_prompt_attn_workspace_bytes(const tb_dims *dims, int32_t n_tokens, int32_t max_new) {
+    if (check_multi_shape(dims, n_tokens, max_new, false, __func__) != TB_OK) return 0;
+    return multi_attn_ws_bytes(*dims, n_tokens, max_new);
+}
+
+size_t tb_tree_attn_workspace_bytes(const tb_dims *dims, int32_t n_tokens, int32_t max_new) {
+    if (check_multi_shape(dims, n_tokens, max_new, true, __func__) != TB_OK) return 0;
+    return multi_attn_ws_bytes(*dims, n_tokens, max_new);
+}
+
+static tb_status multi_attn_impl(const char *fn, bool tree, const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K,
+                                 const tb_bf16 *V, const int32_t *q_begin, int32_t n_tokens, int32_t max_new,
+                                 const int32_t *ctx_len, const uint32_t *mask, float scale, tb_bf16 *out, void *ws,
+                                 size_t ws_bytes, void *stream) {
+    tb_status s;
+    if ((s = check_multi_shape(dims, n_tokens, max_new, tree, fn)) != TB_OK) return s;
+    if (n_tokens == 0) return TB_OK;  // (empty arrays may have no address)
+    TB_CHECK_PTR_IN(Q, fn); TB_CHECK_PTR_IN(K, fn); TB_CHECK_PTR_IN(V, fn); TB_CHECK_PTR_IN(out, fn);
+    TB_CHECK_PTR4_IN(q_begin, fn); TB_CHECK_PTR4_IN(ctx_len, fn);
+    if (tree) TB_CHECK_PTR4_IN(mask, fn);
+    if (!isfinite(scale) || !(scale > 0.f)) return fail(TB_ERR_INVALID_ARG, "%s: scale is not finite and > 0", fn);
+    const size_t qb = (size_t)n_tokens * dims->n_q_heads * dims->head_dim * 2;
+    const size_t kb = (size_t)dims->batch * dims->n_kv_heads * dims->ctx_cap * dims->head_dim * 2;
+    if (overlap(out, qb, Q, qb) || overlap(out, qb, K, kb) || overlap(out, qb, V, kb))
+        return fail(TB_ERR_INVALID_ARG, "%s: out overlaps Q, K or V", fn);
+    if ((s = check_ws(ws, ws_bytes, multi_attn_ws_bytes(*dims, n_tokens, max_new), fn)) != TB_OK) return s;
+    return cuda_status(launch_multi_attn(*dims, Q, K, V, q_begin, n_tokens, max_new, ctx_len, tree ? mask : nullptr,
+                                         scale, out, ws, (cudaStream_t)stream),
+                       fn);
+}
+
+tb_status tb_prompt_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, const tb_bf16 *V,
+                         const int32_t *q_begin, int32_t n_tokens, int32_t max_new, const int32_t *ctx_len,
+                         float scale, tb_bf16 *out, void *ws, size_t ws_bytes, void *stream) {
+    return multi_attn_impl(__func__, false, dims, Q, K, V, q_begin, n_tokens, max_new, ctx_len, nullptr, scale, out, ws,
+                           ws_bytes, stream);
+}
+
+tb_status tb_tree_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, const tb_bf16 *V,
+                       const int32_t *q_begin, int32_t n_tokens, int32_t max_new, const int32_t *ctx_len,
+                       const uint32_t *mask, float scale, tb_bf16 *out, void *ws, size_t ws_bytes, void *stream) {
+    return multi_attn_impl(__func__, true, dims, Q, K, V, q_begin, n_tokens, max_new, ctx_len, mask, scale, out, ws,
+                           ws_bytes, stream);
+}
+
+tb_status tb_tree_accept(const tb_dims *dims, int32_t n_layers, const uint64_t *caches, const int32_t *q_begin,
+                         const int32_t *ctx_len, const int32_t *path, int32_t path_cap, const int32_t *path_len,
+                         int32_t *new_len, void *ws, size_t ws_bytes, void *stream) {
+    tb_status s;
+    if ((s = check_dims_multi(dims, __func__)) != TB_OK) return s;
+    if (!caches || (reinterpret_cast<uintptr_t>(caches) & 7u) != 0)
+        return fail(TB_ERR_INVALID_ARG, "%s: caches is null or not 8-byte aligned", __func__);
+    TB_CHECK_PTR4(q_begin); TB_CHECK_PTR4(ctx_len); TB_CHECK_PTR4(path); TB_CHECK_PTR4(path_len); TB_CHECK_PTR4(new_len);
+    if (n_layers < 1 || n_layers > (1 << 20))
+        return fail(TB_ERR_INVALID_ARG, "%s: n_layers %d out of range", __func__, n_layers);
+    if (path_cap < 1 || path_cap > kMaxTree)
+        return fail(TB_ERR_UNSUPPORTED, "%s: path_cap %d outside [1, %d]", __func__, path_cap, kMaxTree);
+    const size_t lens = (size_t)dims->batch * 4;
+    if (overlap(new_len, lens, ctx_len, lens) || overlap(new_len, lens, path_len, lens) ||
+        overlap(new_len, lens, path, lens * path_cap) || overlap(new_len, lens, q_begin, lens + 4))
+        return fail(TB_ERR_INVALID_ARG, "%s: new_len overlaps an input", __func__);
+    if ((s = check_ws(ws, ws_bytes, kWsHeaderBytes, __func__)) != TB_OK) return s;
+    return cuda_status(launch_tree_accept(*dims, n_layers, caches, q_begin, ctx_len, path, path_cap, path_len, new_len,
+                                          ws, (cudaStream_t)stream),
+                       __func__);
 }
 
 tb_status tb_selftest_bounded_wait(void *ws, size_t ws_bytes, int64_t budget_cycles, void *stream) {
