@@ -47,13 +47,14 @@ constexpr int kTile = 128;                  // K/V rows per tile
 constexpr int kThreads = 384;
 // Registers a thread: 168 at launch (384 threads fill the file); the third
 // warpgroup gives most of its share to the two softmax warpgroups
-// (2 * 128 * 216 + 128 * 72 = 384 * 168).
+// (2 * 128 * 224 + 128 * 56 = 384 * 168).
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr int kMaxSplits = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;               // log2 units
 constexpr uint32_t kBarMerge = 1;           // named barrier of the 256 softmax threads
+constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 template <int D>
@@ -64,7 +65,7 @@ struct Lay {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kOperand;
     static constexpr int kBar = kRing + kStages * kOperand;
-    static constexpr int kNumBars = 2 * kStages + 2 + 6;
+    static constexpr int kNumBars = 2 * kStages + 3 + 8;
     static constexpr int kMisc = kBar + kNumBars * 8;
     static constexpr int kBytes = kMisc + 64 + 1024;  // + alignment slack
     static_assert(kBar % 8 == 0, "mbarrier alignment");
@@ -87,6 +88,21 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// One lane of the calling (converged) warp.  Unlike a test of the lane number
+// it tells the compiler that the branch is taken by one thread of a uniform
+// warp, so operands of the instructions inside stay in uniform registers: with
+// `lane == 0` eight products took about 850 cycles to issue, with this less
+// than they take to run (8 x 64).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 // wait_role by a whole warp: one answer for all lanes.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t *flags) {
     return __all_sync(kFullMask, wait_role(bar, parity, abort_flag, flags));
@@ -101,6 +117,59 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Pairs of fp32 in a 64-bit register: one instruction works on both.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// 2^x for a pair on the FMA pipe: x = n + f with n the nearest integer, 2^f by
+// a cubic with the smallest largest relative error on [-1/2, 1/2] (1.02e-4,
+// fitted for this kernel; 2^0 = 1 exactly; the weights' rounding to bf16 is up
+// to 40 times that), n added to the exponent.  x is
+// held at -127 or above, where the result is exactly 0.
+__device__ __forceinline__ void ex2_poly2(uint64_t x2, float &e0, float &e1) {
+    float a, b;
+    unpack2(x2, a, b);
+    const uint64_t x = pack2(fmaxf(a, -127.f), fmaxf(b, -127.f));
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
+    const uint64_t t = add2(x, pack2(kMagic, kMagic));
+    const uint64_t n = add2(t, pack2(-kMagic, -kMagic));
+    const uint64_t f = sub2(x, n);
+    uint64_t r = fma2(f, pack2(0.05500893294811249f, 0.05500893294811249f),
+                      pack2(0.24221095442771912f, 0.24221095442771912f));
+    r = fma2(r, f, pack2(0.6932829022407532f, 0.6932829022407532f));
+    r = fma2(r, f, pack2(1.f, 1.f));
+    float t0, t1, r0, r1;
+    unpack2(t, t0, t1);
+    unpack2(r, r0, r1);
+    e0 = __uint_as_float(__float_as_uint(r0) + (__float_as_uint(t0) << 23));
+    e1 = __uint_as_float(__float_as_uint(r1) + (__float_as_uint(t1) << 23));
+}
+// The largest of three; NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 // two fp32 -> packed bf16 (round to nearest even), `lo` in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -117,14 +186,30 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// D(tmem) (+)= A(tmem) * B(smem desc)^T, issued by one thread.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The two products' tcgen05.mma, issued by one thread.  Of a shared-memory
+// descriptor only the low word varies (start address; the leading byte offset
+// is the same for every operand here), so the callers step 32-bit words.
+// D(tmem) (+)= A(smem) * B(smem)^T, both K-major.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D(tmem) (+)= A(tmem) * B(smem), B MN-major.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -241,12 +326,12 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     auto bar = [&](int i) -> uint32_t { return sb + L::kBar + 8u * (uint32_t)i; };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(L::kStages + s); };
-    const uint32_t q_full = bar(2 * L::kStages), drain = bar(2 * L::kStages + 1);
-    auto s_full = [&](int s) { return bar(2 * L::kStages + 2 + s); };
-    auto p_full = [&](int s) { return bar(2 * L::kStages + 4 + s); };
-    auto o_done = [&](int s) { return bar(2 * L::kStages + 6 + s); };
+    const uint32_t q_full = bar(2 * L::kStages), drain = bar(2 * L::kStages + 1), tail_done = bar(2 * L::kStages + 2);
+    auto s_full = [&](int s) { return bar(2 * L::kStages + 3 + s); };
+    auto p_full = [&](int s, int half) { return bar(2 * L::kStages + 5 + 2 * s + half); };  // keys 0..63, 64..127
+    auto o_done = [&](int s) { return bar(2 * L::kStages + 9 + s); };
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFullMask, tid >> 5, 0);
     griddep_wait();
     griddep_launch_dependents();
 
@@ -275,6 +360,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const int nt = t_last - t_first;
     const int nt0 = pair ? max(0, min(t_last, tiles_upto(p, it, it.tok0 + tps - 1)) - t_first) : (nt + 1) / 2;
     const int nt1 = pair ? nt : nt / 2;
+    // rows of the CTA's last tile that lie below the length, if not all do (else 0)
+    const int tail_rows = nt > 0 && t_last * kTile > it.T ? it.T - (t_last - 1) * kTile : 0;
 
     if (tid == 0) {
         for (int s = 0; s < L::kStages; ++s) {
@@ -283,9 +370,11 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
         mbar_init(q_full, 1);
         mbar_init(drain, 1);
+        mbar_init(tail_done, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full(s), 1);
-            mbar_init(p_full(s), 4);
+            mbar_init(p_full(s, 0), 4);
+            mbar_init(p_full(s, 1), 4);
             mbar_init(o_done(s), 1);
         }
         misc[1] = 0;
@@ -310,6 +399,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // ============================================================ loads
         // Ring order = the order in which the products use the tiles: in
         // pairs K0 V0 K1 V1 ..; else K0 K1 V0 K2 V1 .. V(n-2) V(n-1).
+        int n_issued = 0;
         if (lane == 0) {
             prefetch_tensormap(&tmQ);
             prefetch_tensormap(&tmK);
@@ -347,90 +437,104 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (ok && t + 2 < nt) load(&tmK, t + 2);
                 }
             }
-            // leave only when every copy has landed (on the normal path the
-            // products have waited for each of them already)
             mbar_wait_bounded(q_full, 0, p.flags);
-            for (int k = max(0, i - L::kStages); k < i; ++k)
-                mbar_wait_bounded(full(k % L::kStages), (k / L::kStages) & 1, p.flags);
+            n_issued = i;
         }
-        __syncwarp();
-    } else if (warp == 8) {
+        n_issued = __shfl_sync(kFullMask, n_issued, 0);
+        // leave only when every copy has landed
+        for (int k = max(0, n_issued - L::kStages); k < n_issued; ++k)
+            mbar_wait_bounded(full(k % L::kStages), (k / L::kStages) & 1, p.flags);
+        if (tail_rows > 0) {
+            // the last V tile (the ring's last item) reaches past the length:
+            // cache rows there may hold anything, NaN included, and 0 * NaN
+            // must not reach the sums
+            uint8_t *v = sm + L::kRing + ((2 * nt - 1) % L::kStages) * L::kOperand;
+            if (n_issued == 2 * nt) {
+#pragma unroll
+                for (int a = 0; a < L::kAtoms; ++a)
+                    for (int o = tail_rows * 128 + lane * 16; o < kTile * 128; o += 512)
+                        *reinterpret_cast<uint4 *>(v + a * 16384 + o) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tail_done);
+        }
+        }
+        if (warp == 8) {
         // ============================================================ products
-        // step i belongs to slot i & 1; in pairs both slots' steps 2t, 2t+1
-        // use tile t, else step i uses tile i.  The order is S(0) S(1), then
-        // PV(i) S(i+2): S(i+2) overwrites P(i), which PV(i) has read (the
-        // products of one thread run in order).
-        const uint32_t id_s = idesc_bf16_f32(128, kTile);
-        const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
-        const int steps = pair ? 2 * nt : nt;
-        int item = 0, k_stage = 0, v_stage = 0;
-        bool ok = wait_warp(q_full, 0, abort_flag, p.flags);
-        auto acquire = [&](int &stage) {
-            stage = item % L::kStages;
-            if (ok) ok = wait_warp(full(stage), (item / L::kStages) & 1, abort_flag, p.flags);
-            ++item;
-        };
-        auto issue_s = [&](int i) {
-            if (!ok || i >= steps) return;
-            const int slot = i & 1, j = i >> 1;
-            const bool first = !pair || slot == 0, last = !pair || slot == 1;
-            if (first) acquire(k_stage);
-            if (!ok) return;
-            if (lane == 0) {
-                if (j < (slot ? nt1 : nt0)) {
-                    tc_fence_after();
-                    const uint32_t q = sb + (pair ? slot : 0) * L::kOperand, k = sb + L::kRing + k_stage * L::kOperand;
+        // One thread issues all of them.  Per slot the order is S(0), then
+        // PV(j) S(j+1): S(j+1) overwrites the columns of P(j), which PV(j)
+        // has read by then (the products of one thread run in order).  PV is
+        // issued in two halves of 64 keys, so that its first half runs while
+        // the softmax works out the second half of the weights.
+        if (elect_one()) {
+            constexpr uint32_t id_s = idesc_bf16_f32(128, kTile);
+            constexpr uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
+            constexpr uint32_t kStep = L::kOperand >> 4;
+            const uint64_t kd = sw128_kmajor_desc(sb), vd = sw128_mnmajor_desc(sb + L::kRing, 16384);
+            const uint32_t q_lo = (uint32_t)kd, hi = (uint32_t)(kd >> 32);
+            const uint32_t k_lo = q_lo + (L::kRing >> 4), v_lo = (uint32_t)vd;
+            int k_stage = 0, v_stage = 0, next = 0;
+            uint32_t next_parity = 0;
+            bool ok = wait_role(q_full, 0, abort_flag, p.flags);
+            auto acquire = [&](int &stage) {
+                stage = next;
+                if (ok) ok = wait_role(full(next), next_parity, abort_flag, p.flags);
+                if (++next == L::kStages) {
+                    next = 0;
+                    next_parity ^= 1u;
+                }
+            };
+            auto issue_s = [&](int slot) {
+                tc_fence_after();
+                const uint32_t q = q_lo + (pair ? slot : 0) * kStep, k = k_lo + k_stage * kStep;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t o = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-                        umma_bf16(tmem + slot * 128, sw128_kmajor_desc(q + o), sw128_kmajor_desc(k + o), id_s, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (uint32_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+                    umma_ss(tmem + slot * 128, q + o, k + o, hi, id_s, kk > 0);
+                }
+                umma_commit(s_full(slot));
+            };
+            auto issue_pv = [&](int slot, int j) {
+                const uint32_t v = v_lo + v_stage * kStep;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (ok) ok = wait_role(p_full(slot, half), j & 1, abort_flag, p.flags);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                        umma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, v + kk * 128, hi, id_o,
+                                (j | kk) ? 1u : 0u);
+                }
+                umma_commit(o_done(slot));
+            };
+            // step i belongs to slot i & 1; in pairs steps 2t and 2t + 1 use
+            // tile t, else step i uses tile i.  Each round: the step's PV,
+            // then the same slot's next S.
+            const int steps = pair ? 2 * nt : nt;
+#pragma unroll 1
+            for (int i = -2; i < steps && ok; ++i) {
+                const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
+                const bool first = !pair || slot == 0, last = !pair || slot == 1;
+                if (i >= 0) {
+                    if (first) {
+                        acquire(v_stage);
+                        if (tail_rows > 0 && (pair ? j : i) + 1 == nt && ok)
+                            ok = wait_role(tail_done, 0, abort_flag, p.flags);
                     }
-                    umma_commit(s_full(slot));
+                    if (j < n_slot) issue_pv(slot, j);
+                    if (!ok) break;
+                    if (last) umma_commit(empty(v_stage));
                 }
-                if (last) umma_commit(empty(k_stage));
-            }
-            __syncwarp();
-        };
-        issue_s(0);
-        issue_s(1);
-        for (int i = 0; i < steps && ok; ++i) {
-            const int slot = i & 1, j = i >> 1, tile = t_first + (pair ? j : i);
-            const bool first = !pair || slot == 0, last = !pair || slot == 1;
-            if (first) {
-                acquire(v_stage);
-                // cache rows at and past the length may hold anything, NaN
-                // included: 0 * NaN must not reach the sums
-                const int rows = it.T - tile * kTile;
-                if (ok && rows < kTile) {
-                    uint8_t *v = sm + L::kRing + v_stage * L::kOperand;
-#pragma unroll
-                    for (int a = 0; a < L::kAtoms; ++a)
-                        for (int o = max(rows, 0) * 128 + lane * 16; o < kTile * 128; o += 512)
-                            *reinterpret_cast<uint4 *>(v + a * 16384 + o) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                if (i + 2 < steps) {
+                    if (first) acquire(k_stage);
+                    if (!ok) break;
+                    if (j + 1 < n_slot) issue_s(slot);
+                    if (last) umma_commit(empty(k_stage));
                 }
             }
-            if (!ok) break;
-            if (j < (slot ? nt1 : nt0)) {
-                ok = wait_warp(p_full(slot), j & 1, abort_flag, p.flags);
-                if (!ok) break;
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint32_t v = sb + L::kRing + v_stage * L::kOperand;
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_bf16_ta(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8,
-                                     sw128_mnmajor_desc(v + kk * 2048, 16384), id_o, (j | kk) ? 1u : 0u);
-                    umma_commit(o_done(slot));
-                }
-            }
-            if (last && lane == 0) umma_commit(empty(v_stage));
-            __syncwarp();
-            issue_s(i + 2);
-        }
-        if (lane == 0) {  // no product is in flight when the CTA ends
-            umma_commit(drain);
+            umma_commit(drain);  // no product is in flight when the CTA ends
             mbar_wait_bounded(drain, 0, p.flags);
         }
         __syncwarp();
@@ -446,8 +550,11 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int tok = it.tok0 + ((pair ? slot : 0) * tps) + (row >> p.g_shift);
         const bool live = tok < it.tok0 + it.ntok;
         const int base = it.T - it.n;  // first row of the new tokens
-        const int lim = base + tok;    // causal: the last row this token sees
-        const uint32_t *mrow = p.mask ? p.mask + (size_t)(it.begin + (live ? tok : it.tok0)) * p.mask_words : nullptr;
+        // the row sees every cache row below all_end, and of the drafted rows
+        // from all_end to draft_end those with a bit in mrow
+        const uint32_t *mrow = p.mask && live ? p.mask + (size_t)(it.begin + tok) * p.mask_words : nullptr;
+        const int all_end = !live ? 0 : p.mask ? base : base + tok + 1;
+        const int draft_end = base + min(it.n, p.max_new);
         const int n_mine = slot ? nt1 : nt0;
         // tiles from `masked_from` on hold rows that some row of this slot does not see
         const int masked_from = p.mask ? max(base, 0) / kTile
@@ -457,20 +564,20 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
         // which of the 32 cache rows from p0 on this row attends to
         auto allowed = [&](int p0) -> uint32_t {
-            if (!live) return 0u;
-            if (!mrow) return bits_below(lim + 1 - p0);
-            const uint32_t prefix = bits_below(base - p0);
-            const int j0 = p0 - base;  // drafted token at p0
-            uint32_t d = 0u;
-            if (j0 <= -32) {
-            } else if (j0 < 0) {
-                d = __ldg(mrow) << -j0;
-            } else if ((j0 >> 5) < p.mask_words) {
-                const int w = j0 >> 5, sh = j0 & 31;
-                d = __ldg(mrow + w) >> sh;
-                if (sh && w + 1 < p.mask_words) d |= __ldg(mrow + w + 1) << (32 - sh);
+            uint32_t d = bits_below(all_end - p0);
+            if (mrow) {
+                const int j0 = p0 - all_end;  // drafted token at p0
+                uint32_t x = 0u;
+                if (j0 >= 0) {
+                    const int w = j0 >> 5, sh = j0 & 31;
+                    if (w < p.mask_words) x = __ldg(mrow + w) >> sh;
+                    if (sh && w + 1 < p.mask_words) x |= __ldg(mrow + w + 1) << (32 - sh);
+                } else if (j0 > -32) {
+                    x = __ldg(mrow) << -j0;
+                }
+                d |= x & bits_below(draft_end - p0);
             }
-            return prefix | (d & bits_below(base + min(it.n, p.max_new) - p0));
+            return d;
         };
 
         for (int j = 0; j < n_mine; ++j) {
@@ -496,16 +603,23 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int k = 0; k < 32; ++k)
                         if (!((see[q] >> k) & 1u)) s[q][k] = 0xff800000u;  // -inf
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[4];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
+            for (int q = 0; q < 4; ++q) mx[q] = max3_nan(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][k]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
-            const bool raise = top > m + kLazy;  // also the first logit of a row (m = -inf)
+            for (int k = 3; k < 31; k += 2)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mx[q] = max3_nan(mx[q], __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = max3_nan(mx[q], __uint_as_float(s[q][31]), mx[q]);
+            float top = max3_nan(mx[0], mx[1], max3_nan(mx[2], mx[3], mx[3])) * p.c;
+            // a NaN or +inf logit makes the row's softmax NaN: so becomes m, and l with it
+            if (!(top < INFINITY)) top = NAN;
+            const bool raise = !(top <= m + kLazy);  // also the first logit of a row (m = -inf)
             if (__any_sync(kFullMask, raise)) {
                 const float m_new = raise ? top : m;
-                const float f = raise ? ex2(m - m_new) : 1.f;
+                const float f = m_new == m ? 1.f : ex2(m - m_new);  // (-inf stays -inf while nothing is seen)
                 if (j > 0) {
                     ok = wait_warp(o_done(slot), (j - 1) & 1, abort_flag, p.flags);
                     if (!ok) break;
@@ -524,26 +638,38 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 m = m_new;
             }
             const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: 2^(-inf - 0) = 0
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t c2 = pack2(p.c, p.c), nm2 = pack2(-mm, -mm);
+            uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t w[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const float e0 = ex2(fmaf(__uint_as_float(s[q][2 * k]), p.c, -mm));
-                    const float e1 = ex2(fmaf(__uint_as_float(s[q][2 * k + 1]), p.c, -mm));
-                    sum[q] += e0 + e1;
+                    const uint64_t x2 = fma2(pack2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), c2, nm2);
+                    float e0, e1;
+                    if ((k & 7) < kPolyOf8) {
+                        ex2_poly2(x2, e0, e1);
+                    } else {
+                        unpack2(x2, e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                    }
+                    sum2[k & 1] = add2(sum2[k & 1], pack2(e0, e1));
                     // rounded to bf16 for the second product: 2^-9 relative per
                     // weight, below the rounding of the bf16 result
                     w[k] = pack_bf16(e0, e1);
                 }
                 tmem_st16(ts + q * 16, w);
+                if (q & 1) {  // half of the weights are in place
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(slot, q >> 1));
+                }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(slot));
+            float u0, u1;
+            unpack2(add2(sum2[0], sum2[1]), u0, u1);
+            l += u0 + u1;
         }
 
         // ---- epilogue
