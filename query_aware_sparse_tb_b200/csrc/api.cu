@@ -415,12 +415,12 @@ static tb_status check_multi_shape(const tb_dims *dims, int32_t n_tokens, int32_
 
 size_t tb_prompt_attn_workspace_bytes(const tb_dims *dims, int32_t n_tokens, int32_t max_new) {
     if (check_multi_shape(dims, n_tokens, max_new, false, __func__) != TB_OK) return 0;
-    return multi_attn_ws_bytes(*dims, n_tokens, max_new);
+    return multi_attn_ws_bytes(*dims, n_tokens, max_new, false);
 }
 
 size_t tb_tree_attn_workspace_bytes(const tb_dims *dims, int32_t n_tokens, int32_t max_new) {
     if (check_multi_shape(dims, n_tokens, max_new, true, __func__) != TB_OK) return 0;
-    return multi_attn_ws_bytes(*dims, n_tokens, max_new);
+    return multi_attn_ws_bytes(*dims, n_tokens, max_new, true);
 }
 
 static tb_status multi_attn_impl(const char *fn, bool tree, const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K,
@@ -438,7 +438,7 @@ static tb_status multi_attn_impl(const char *fn, bool tree, const tb_dims *dims,
     const size_t kb = (size_t)dims->batch * dims->n_kv_heads * dims->ctx_cap * dims->head_dim * 2;
     if (overlap(out, qb, Q, qb) || overlap(out, qb, K, kb) || overlap(out, qb, V, kb))
         return fail(TB_ERR_INVALID_ARG, "%s: out overlaps Q, K or V", fn);
-    if ((s = check_ws(ws, ws_bytes, multi_attn_ws_bytes(*dims, n_tokens, max_new), fn)) != TB_OK) return s;
+    if ((s = check_ws(ws, ws_bytes, multi_attn_ws_bytes(*dims, n_tokens, max_new, tree), fn)) != TB_OK) return s;
     return cuda_status(launch_multi_attn(*dims, Q, K, V, q_begin, n_tokens, max_new, ctx_len, tree ? mask : nullptr,
                                          scale, out, ws, (cudaStream_t)stream),
                        fn);

@@ -12,7 +12,7 @@
 namespace tb {
 
 // ---- prompt and tree attention (multi_attn.cu) ----
-size_t multi_attn_ws_bytes(const tb_dims &d, int32_t n_tokens, int32_t max_new);
+size_t multi_attn_ws_bytes(const tb_dims &d, int32_t n_tokens, int32_t max_new, bool tree);
 // mask == nullptr: causal; else the tree's attention bits [n_tokens][ceil(max_new/32)].
 cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
                               const int32_t *q_begin, int32_t n_tokens, int32_t max_new, const int32_t *ctx_len,

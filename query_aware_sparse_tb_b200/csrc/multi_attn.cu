@@ -23,16 +23,23 @@
 // at the end), so short items keep both warpgroups busy too.
 //
 // Warps: 0-3 softmax of slot 0, 4-7 softmax of slot 1, 8 issues the products,
-// 9 loads (TMA); 10 and 11 only complete the warpgroup whose registers the
-// softmax warps take over (a softmax thread holds a whole row of a tile, 128
-// logits).  Tensor memory: S0 | S1 | O0 | O1, 128 columns each; the
-// weights P (bf16) overwrite the first half of their S columns and are read
-// from there as the A operand of the second product.
+// 9 loads (TMA), 10 schedules; 11 only completes the warpgroup whose registers
+// the softmax warps take over (a softmax thread holds a whole row of a tile,
+// 128 logits).  Tensor memory: S0 | S1 | O0 | O1, 128 columns each; the weights
+// P (bf16) overwrite the first half of their S columns and are read from there
+// as the A operand of the second product.
 //
-// Few items over a long context are split along it (gridDim covers
-// splits x items); each CTA then writes its rows' unnormalised state and a
-// second kernel joins them.
+// The grid is one CTA per SM, each working through a list of segments (an item
+// or a part of its K/V tiles) that warp 10 describes to the other warps one
+// segment ahead, so the next segment's loads and first products overlap the
+// end of the current one.  Two ways to deal the work out, chosen on the host:
+//   - many items: a counter, longest items of each sequence first;
+//   - few items over long contexts: all tiles of all items in one line, cut
+//     into equal shares.  A CTA's share may begin and end inside an item; such
+//     parts leave their rows' unnormalised state in the workspace and a second
+//     kernel joins them.
 #include <cuda.h>
+#include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -50,10 +57,8 @@ constexpr int kThreads = 384;
 // (2 * 128 * 224 + 128 * 56 = 384 * 168).
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
-constexpr int kMaxSplits = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;               // log2 units
-constexpr uint32_t kBarMerge = 1;           // named barrier of the 256 softmax threads
 constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
 constexpr uint32_t kFullMask = 0xffffffffu;
 
@@ -65,9 +70,11 @@ struct Lay {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kOperand;
     static constexpr int kBar = kRing + kStages * kOperand;
-    static constexpr int kNumBars = 2 * kStages + 3 + 8;
-    static constexpr int kMisc = kBar + kNumBars * 8;
-    static constexpr int kBytes = kMisc + 64 + 1024;  // + alignment slack
+    static constexpr int kNumBars = 2 * kStages + 20;
+    static constexpr int kMisc = kBar + kNumBars * 8;       // TMEM base, abort flag
+    static constexpr int kSeg = (kMisc + 8 + 15) / 16 * 16; // two segment descriptions
+    static constexpr int kState = kSeg + 2 * 64;            // the slots' m and l [2 slots][2][128]
+    static constexpr int kBytes = kState + 2048;
     static_assert(kBar % 8 == 0, "mbarrier alignment");
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -75,7 +82,7 @@ struct Lay {
 // A bounded mbarrier wait that also gives up as soon as another role of the
 // CTA has given up.  The thread sleeps in the barrier between checks.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t *flags) {
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     for (;;) {
         if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
@@ -248,33 +255,73 @@ struct Params {
     const int32_t *q_begin, *ctx_len;
     const uint32_t *mask;   // nullptr: causal
     uint16_t *out;
-    float *part;            // split states, nullptr when splits == 1
-    uint32_t *flags;
+    float *part;            // shares: two states per CTA; nullptr: the counter deals whole items out
+    int32_t *joins;         // shares: one entry per CTA (the item that ends in its first segment)
+    uint32_t *flags, *counter;  // counter[0]: next item, counter[1]: CTAs done
     int batch, Hq, Hkv, cap, n_tokens, max_new, mask_words;
     int g_shift;            // G = 1 << g_shift heads per group
-    int item_bound, splits;
+    int item_bound;         // items of a KV head, at most
     float c;                // scale * log2(e)
 };
 
-// One work item: up to 256 rows (tokens tok0 .. tok0 + ntok of sequence b).
-struct Item {
-    int b, begin, n, T;  // the sequence: first packed token, new tokens, length
-    int tok0, ntok;      // tokens of this item (index within the sequence)
-    int index;           // among all items of a KV head
-    bool any;
+// A segment as warp 10 describes it to the others.
+enum SegField {
+    kEnd,        // 1: no further segment
+    kPair,       // slots: 1 = two row blocks over the same tiles, 0 = one row block, every other tile
+    kRowBase,    // first cache row of the (sequence, KV head)
+    kTok,        // packed index of the item's first token
+    kHead,       // first query head of the group
+    kNTok,       // tokens of the item
+    kLen,        // T
+    kBase,       // T - n, the first new token's cache row
+    kTok0,       // the item's first token within the sequence
+    kDraftEnd,   // end of the drafted rows the mask covers
+    kFirst,      // first K/V tile
+    kTiles,      // tiles
+    kTiles0,     // tiles of slot 0
+    kTiles1,     // tiles of slot 1
+    kTail,       // rows of the last tile below the length, if not all are (else 0)
+    kPart,       // state to write, -1: the result itself
+    kSegFields
 };
+static_assert(kSegFields * 4 <= 64, "segment description");
 
-// Item `tau` counted over the sequences in packing order.  Every lane of the
-// calling warp takes part; sequences with more than max_new tokens keep
-// max_new (the rest is reported and left out).
-__device__ __forceinline__ Item find_item(const Params &p, int tau, int lane) {
-    const int tpi_shift = 8 - p.g_shift;  // tokens per item: 256 / G
-    Item it{};
+// The new tokens of one sequence (n clamped to max_new for the items).
+struct Seq {
+    int b, begin, n, kept, T;
+};
+__device__ __forceinline__ Seq load_seq(const Params &p, int b) {
+    Seq q;
+    q.b = b;
+    const SeqSpan sp = seq_span(p.q_begin, b, p.n_tokens);
+    q.begin = sp.begin;
+    q.n = sp.n;
+    q.kept = min(sp.n, p.max_new);
+    q.T = sp.n > 0 ? clamp_ctx(p.ctx_len[b], p.cap, nullptr, false) : 0;
+    return q;
+}
+__device__ __forceinline__ int items_of(const Params &p, int kept) {
+    const int tpi = kItemRows >> p.g_shift;
+    return (kept + tpi - 1) / tpi;
+}
+// K/V tiles that the sequence's tokens up to `last` attend to.
+__device__ __forceinline__ int tiles_upto(const Params &p, const Seq &q, int last) {
+    const int rows = p.mask ? q.T : min(q.T, q.T - q.n + last + 1);
+    return max(0, (rows + kTile - 1) / kTile);
+}
+__device__ __forceinline__ int item_tiles(const Params &p, const Seq &q, int item) {
+    const int tpi = kItemRows >> p.g_shift;
+    return tiles_upto(p, q, min((item + 1) * tpi, q.kept) - 1);
+}
+
+// All lanes of a warp: sequence and number within it of item `tau`, counted
+// over the sequences in packing order.
+__device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, int &b, int &item) {
     int before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         int n = 0;
         if (b0 + lane < p.batch) n = min(seq_span(p.q_begin, b0 + lane, p.n_tokens).n, p.max_new);
-        const int items = (n + (1 << tpi_shift) - 1) >> tpi_shift;
+        const int items = items_of(p, n);
         int incl = items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -284,105 +331,95 @@ __device__ __forceinline__ Item find_item(const Params &p, int tau, int lane) {
         const uint32_t hit = __ballot_sync(kFullMask, tau < before + incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int first = before + __shfl_sync(kFullMask, incl - items, l);
-            it.b = b0 + l;
-            const SeqSpan sp = seq_span(p.q_begin, it.b, p.n_tokens);
-            it.begin = sp.begin;
-            it.n = sp.n;
-            it.tok0 = (tau - first) << tpi_shift;
-            it.ntok = min(1 << tpi_shift, min(sp.n, p.max_new) - it.tok0);
-            it.index = tau;
-            it.any = true;
-            return it;
+            b = b0 + l;
+            item = tau - before - __shfl_sync(kFullMask, incl - items, l);
+            return true;
         }
         before += __shfl_sync(kFullMask, incl, 31);
     }
-    return it;
+    return false;
 }
 
-// K/V tiles that tokens up to `last` of the item's sequence attend to.
-__device__ __forceinline__ int tiles_upto(const Params &p, const Item &it, int last) {
-    const int rows = p.mask ? it.T : min(it.T, it.T - it.n + last + 1);
-    return max(0, (rows + kTile - 1) / kTile);
+// Shares: the tiles of all items in one line (sequences in packing order, its
+// items in order, KV heads inside an item).  All lanes of a warp.  Tiles of
+// one sequence over all its items and KV heads:
+__device__ __forceinline__ long long seq_tiles(const Params &p, int b) {
+    const Seq q = load_seq(p, b);
+    const int items = items_of(p, q.kept);
+    long long t = 0;
+    if (p.mask) {
+        t = (long long)items * tiles_upto(p, q, 0);
+    } else {
+        for (int i = 0; i < items; ++i) t += item_tiles(p, q, i);
+    }
+    return t * p.Hkv;
 }
-
-// Tiles of split s of an item with `tiles` tiles: [first, last).
-__device__ __forceinline__ void split_range(int tiles, int splits, int s, int &first, int &last) {
-    const int per = (tiles + splits - 1) / splits;
-    first = min(s * per, tiles);
-    last = min(first + per, tiles);
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
 }
+__device__ __forceinline__ long long share_begin(long long total, int c, int ctas) { return total * c / ctas; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
     using L = Lay<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_addr(sm);
-    volatile int *misc = reinterpret_cast<volatile int *>(sm + L::kMisc);  // TMEM base, abort flag, item
+    if (sb & 1023u) {  // the operands' layout needs it; no room is left to align here
+        if (threadIdx.x == 0) raise_flag(p.flags, TB_FLAG_TIMEOUT);
+        return;
+    }
+    volatile int *misc = reinterpret_cast<volatile int *>(sm + L::kMisc);
     volatile int *abort_flag = misc + 1;
     auto bar = [&](int i) -> uint32_t { return sb + L::kBar + 8u * (uint32_t)i; };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(L::kStages + s); };
-    const uint32_t q_full = bar(2 * L::kStages), drain = bar(2 * L::kStages + 1), tail_done = bar(2 * L::kStages + 2);
-    auto s_full = [&](int s) { return bar(2 * L::kStages + 3 + s); };
-    auto p_full = [&](int s, int half) { return bar(2 * L::kStages + 5 + 2 * s + half); };  // keys 0..63, 64..127
-    auto o_done = [&](int s) { return bar(2 * L::kStages + 9 + s); };
+    constexpr int kB = 2 * L::kStages;
+    const uint32_t q_full = bar(kB), q_empty = bar(kB + 1), drain = bar(kB + 3);
+    const uint32_t o_free = bar(kB + 4);
+    auto seg_full = [&](int i) { return bar(kB + 5 + i); };
+    auto seg_empty = [&](int i) { return bar(kB + 7 + i); };
+    const uint32_t state_full = bar(kB + 9), state_empty = bar(kB + 10);
+    auto s_full = [&](int s) { return bar(kB + 11 + s); };
+    auto p_full = [&](int s, int half) { return bar(kB + 13 + 2 * s + half); };  // keys 0..63, 64..127
+    auto o_done = [&](int s) { return bar(kB + 17 + s); };
+    auto tail_done = [&](int i) { return bar(i ? kB + 19 : kB + 2); };
+    auto seg = [&](int i) { return reinterpret_cast<volatile int *>(sm + L::kSeg + i * 64); };
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFullMask, tid >> 5, 0);
-    griddep_wait();
-    griddep_launch_dependents();
-
-    // grid: items from the last to the first (a sequence's last tokens have
-    // the most tiles, so the long items start first), KV heads and splits inside
-    const int per_item = p.Hkv * p.splits;
-    const int tau = p.item_bound - 1 - (int)(blockIdx.x / per_item);
-    const int rem = (int)(blockIdx.x % per_item);
-    const int g = rem / p.splits, split = rem % p.splits;
-    Item it = find_item(p, tau, lane);
-    if (!it.any) return;
-    const bool report = tid == 0 && g == 0 && split == 0;
-    it.T = clamp_ctx(p.ctx_len[it.b], p.cap, p.flags, report);
-    if (report && (it.n > it.T || it.n > p.max_new)) raise_flag(p.flags, TB_FLAG_CTX_RANGE);
-
-    // Two ways to use the slots: `pair`: rows 0..127 and 128..255 over the
-    // same tiles; else both slots hold rows 0..127 and take every other tile.
-    const int tps = kSlotRows >> p.g_shift;  // tokens per slot
-    const bool pair = it.ntok > tps;
-    const int tiles_item = tiles_upto(p, it, it.tok0 + it.ntok - 1);
-    int t_first, t_last;
-    split_range(tiles_item, p.splits, split, t_first, t_last);
-    if (p.splits > 1 && t_first >= t_last) return;  // the join skips empty splits
-    // tiles of the whole CTA and of slot 0 (in pairs its rows, the earlier
-    // tokens, may end a tile or two before slot 1's)
-    const int nt = t_last - t_first;
-    const int nt0 = pair ? max(0, min(t_last, tiles_upto(p, it, it.tok0 + tps - 1)) - t_first) : (nt + 1) / 2;
-    const int nt1 = pair ? nt : nt / 2;
-    // rows of the CTA's last tile that lie below the length, if not all do (else 0)
-    const int tail_rows = nt > 0 && t_last * kTile > it.T ? it.T - (t_last - 1) * kTile : 0;
-
     if (tid == 0) {
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         mbar_init(drain, 1);
-        mbar_init(tail_done, 1);
+        mbar_init(o_free, 8);
+        mbar_init(state_full, 8);
+        mbar_init(state_empty, 8);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(seg_full(s), 1);
+            mbar_init(seg_empty(s), 10);
+            mbar_init(tail_done(s), 1);
             mbar_init(s_full(s), 1);
             mbar_init(p_full(s, 0), 4);
             mbar_init(p_full(s, 1), 4);
             mbar_init(o_done(s), 1);
         }
         misc[1] = 0;
-        misc[2] = it.begin + it.tok0;  // what only the epilogue needs: kept out of the loop's registers
-        misc[3] = it.ntok;
-        misc[4] = it.index;
         fence_mbar_init();
     }
+    if (warp == 9 && lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
     if (warp == 8) {
         tmem_alloc(sb + L::kMisc, kTmemCols);
         tmem_relinquish();
@@ -391,153 +428,340 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[0];
-    const int row_base = (int)(((size_t)it.b * p.Hkv + g) * (size_t)p.cap);  // < 2^31 (checked on the host)
+    const int tps = kSlotRows >> p.g_shift;  // tokens per slot
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsOther));
-        if (warp == 9) {
-        // ============================================================ loads
-        // Ring order = the order in which the products use the tiles: in
-        // pairs K0 V0 K1 V1 ..; else K0 K1 V0 K2 V1 .. V(n-2) V(n-1).
-        int n_issued = 0;
-        if (lane == 0) {
-            prefetch_tensormap(&tmQ);
-            prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
-            const int qn = pair ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, (uint32_t)(qn * L::kOperand));
-            for (int s = 0; s < qn; ++s)
-#pragma unroll
-                for (int a = 0; a < L::kAtoms; ++a)
-                    tma_load_3d(sb + s * L::kOperand + a * 16384, &tmQ, q_full, a * 64, g << p.g_shift,
-                                it.begin + it.tok0 + s * tps);
-            int i = 0;
+        if (warp == 10) {
+            // ======================================================== schedule
+            int k = 0;  // segments described so far
             bool ok = true;
-            auto load = [&](const CUtensorMap *map, int tile) {
-                const int s = i % L::kStages;
-                if (i >= L::kStages) ok = ok && wait_role(empty(s), ((i / L::kStages) + 1) & 1, abort_flag, p.flags);
-                if (!ok) return;
-                mbar_arrive_expect_tx(full(s), L::kOperand);
-#pragma unroll
-                for (int a = 0; a < L::kAtoms; ++a)
-                    tma_load_2d(sb + L::kRing + s * L::kOperand + a * 16384, map, full(s), a * 64,
-                                row_base + (t_first + tile) * kTile);
-                ++i;
+            // what only the device sees: reported once per sequence
+            auto report = [&](const Seq &q) {
+                const int t = p.ctx_len[q.b];
+                if (lane == 0 && (t < 1 || t > p.cap || q.n > q.T || q.n > p.max_new)) raise_flag(p.flags, TB_FLAG_CTX_RANGE);
             };
-            if (pair) {
-                for (int t = 0; t < nt && ok; ++t) {
-                    load(&tmK, t);
-                    if (ok) load(&tmV, t);
+            // an item whose tokens see no cache row at all (more new tokens than rows)
+            auto zero_item = [&](const Seq &q, int item, int g) {
+                const int tok0 = item * 2 * tps, ntok = min(2 * tps, q.kept - tok0), per = (D / 8) << p.g_shift;
+                for (int i = lane; i < ntok * per; i += 32)
+                    reinterpret_cast<uint4 *>(p.out + ((size_t)(q.begin + tok0 + i / per) * p.Hq + (g << p.g_shift)) * D)[i % per] =
+                        make_uint4(0, 0, 0, 0);
+            };
+            // tiles [first, last), at least one, of item `item` of sequence q for KV head g
+            auto emit = [&](const Seq &q, int item, int g, int first, int last, int part) {
+                if (k >= 2) ok = wait_warp(seg_empty(k & 1), ((k >> 1) + 1) & 1, abort_flag, p.flags);
+                if (!ok) return;
+                if (lane == 0) {
+                    const int tok0 = item * 2 * tps, ntok = min(2 * tps, q.kept - tok0), nt = last - first;
+                    const bool pair = ntok > tps;
+                    volatile int *f = seg(k & 1);
+                    f[kEnd] = 0;
+                    f[kPair] = pair;
+                    f[kRowBase] = (int)(((size_t)q.b * p.Hkv + g) * (size_t)p.cap);  // < 2^31 (checked on the host)
+                    f[kTok] = q.begin + tok0;
+                    f[kHead] = g << p.g_shift;
+                    f[kNTok] = ntok;
+                    f[kLen] = q.T;
+                    f[kBase] = q.T - q.n;
+                    f[kTok0] = tok0;
+                    f[kDraftEnd] = q.T - q.n + q.kept;
+                    f[kFirst] = first;
+                    f[kTiles] = nt;
+                    // in pairs slot 0's rows, the earlier tokens, may end a tile or two before slot 1's
+                    f[kTiles0] = pair ? max(0, min(last, tiles_upto(p, q, tok0 + tps - 1)) - first) : (nt + 1) / 2;
+                    f[kTiles1] = pair ? nt : nt / 2;
+                    f[kTail] = nt > 0 && last * kTile > q.T ? q.T - (last - 1) * kTile : 0;
+                    f[kPart] = part;
+                    mbar_arrive(seg_full(k & 1));
+                }
+                __syncwarp();
+                ++k;
+            };
+            if (p.part == nullptr) {
+                // from the last item to the first: a sequence's last tokens have the most tiles
+                while (ok) {
+                    int next = 0;
+                    if (lane == 0) next = (int)atomicAdd(p.counter, 1u);
+                    next = __shfl_sync(kFullMask, next, 0);
+                    if (next >= p.item_bound * p.Hkv) break;
+                    int b, item;
+                    if (!find_item(p, p.item_bound - 1 - next / p.Hkv, lane, b, item)) continue;
+                    const Seq q = load_seq(p, b);
+                    const int g = next % p.Hkv, tiles = item_tiles(p, q, item);
+                    if (item == 0 && g == 0) report(q);
+                    if (tiles > 0)
+                        emit(q, item, g, 0, tiles, -1);
+                    else
+                        zero_item(q, item, g);
                 }
             } else {
-                if (nt > 0) load(&tmK, 0);
-                if (nt > 1) load(&tmK, 1);
-                for (int t = 0; t < nt && ok; ++t) {
-                    load(&tmV, t);
-                    if (ok && t + 2 < nt) load(&tmK, t + 2);
-                }
-            }
-            mbar_wait_bounded(q_full, 0, p.flags);
-            n_issued = i;
-        }
-        n_issued = __shfl_sync(kFullMask, n_issued, 0);
-        // leave only when every copy has landed
-        for (int k = max(0, n_issued - L::kStages); k < n_issued; ++k)
-            mbar_wait_bounded(full(k % L::kStages), (k / L::kStages) & 1, p.flags);
-        if (tail_rows > 0) {
-            // the last V tile (the ring's last item) reaches past the length:
-            // cache rows there may hold anything, NaN included, and 0 * NaN
-            // must not reach the sums
-            uint8_t *v = sm + L::kRing + ((2 * nt - 1) % L::kStages) * L::kOperand;
-            if (n_issued == 2 * nt) {
+                const int cta = blockIdx.x;
+                long long total = 0;
+                for (int b0 = 0; b0 < p.batch; b0 += 32)
+                    total += warp_sum(b0 + lane < p.batch ? seq_tiles(p, b0 + lane) : 0);
+                // no share is below 4 tiles: short contexts keep to fewer CTAs
+                const int ctas = (int)min((long long)gridDim.x, max(1LL, total / 4));
+                long long w = cta < ctas ? share_begin(total, cta, ctas) : total;
+                const long long w1 = cta < ctas ? share_begin(total, cta + 1, ctas) : total;
+                int join_from = -1, join_tok = 0, join_head = 0, join_rows = 0;
+                // the sequence that holds w: `at` is where its line begins
+                long long at = 0;
+                int b = 0;
+                for (int b0 = 0; b0 < p.batch; b0 += 32) {
+                    const long long mine = b0 + lane < p.batch ? seq_tiles(p, b0 + lane) : 0;
+                    long long incl = mine;
 #pragma unroll
-                for (int a = 0; a < L::kAtoms; ++a)
-                    for (int o = tail_rows * 128 + lane * 16; o < kTile * 128; o += 512)
-                        *reinterpret_cast<uint4 *>(v + a * 16384 + o) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tail_done);
-        }
-        }
-        if (warp == 8) {
-        // ============================================================ products
-        // One thread issues all of them.  Per slot the order is S(0), then
-        // PV(j) S(j+1): S(j+1) overwrites the columns of P(j), which PV(j)
-        // has read by then (the products of one thread run in order).  PV is
-        // issued in two halves of 64 keys, so that its first half runs while
-        // the softmax works out the second half of the weights.
-        if (elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16_f32(128, kTile);
-            constexpr uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
-            constexpr uint32_t kStep = L::kOperand >> 4;
-            const uint64_t kd = sw128_kmajor_desc(sb), vd = sw128_mnmajor_desc(sb + L::kRing, 16384);
-            const uint32_t q_lo = (uint32_t)kd, hi = (uint32_t)(kd >> 32);
-            const uint32_t k_lo = q_lo + (L::kRing >> 4), v_lo = (uint32_t)vd;
-            int k_stage = 0, v_stage = 0, next = 0;
-            uint32_t next_parity = 0;
-            bool ok = wait_role(q_full, 0, abort_flag, p.flags);
-            auto acquire = [&](int &stage) {
-                stage = next;
-                if (ok) ok = wait_role(full(next), next_parity, abort_flag, p.flags);
-                if (++next == L::kStages) {
-                    next = 0;
-                    next_parity ^= 1u;
-                }
-            };
-            auto issue_s = [&](int slot) {
-                tc_fence_after();
-                const uint32_t q = q_lo + (pair ? slot : 0) * kStep, k = k_lo + k_stage * kStep;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (uint32_t)((kk >> 2) * 1024 + (kk & 3) * 2);
-                    umma_ss(tmem + slot * 128, q + o, k + o, hi, id_s, kk > 0);
-                }
-                umma_commit(s_full(slot));
-            };
-            auto issue_pv = [&](int slot, int j) {
-                const uint32_t v = v_lo + v_stage * kStep;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (ok) ok = wait_role(p_full(slot, half), j & 1, abort_flag, p.flags);
-                    if (!ok) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                        umma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, v + kk * 128, hi, id_o,
-                                (j | kk) ? 1u : 0u);
-                }
-                umma_commit(o_done(slot));
-            };
-            // step i belongs to slot i & 1; in pairs steps 2t and 2t + 1 use
-            // tile t, else step i uses tile i.  Each round: the step's PV,
-            // then the same slot's next S.
-            const int steps = pair ? 2 * nt : nt;
-#pragma unroll 1
-            for (int i = -2; i < steps && ok; ++i) {
-                const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
-                const bool first = !pair || slot == 0, last = !pair || slot == 1;
-                if (i >= 0) {
-                    if (first) {
-                        acquire(v_stage);
-                        if (tail_rows > 0 && (pair ? j : i) + 1 == nt && ok)
-                            ok = wait_role(tail_done, 0, abort_flag, p.flags);
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long v = __shfl_up_sync(kFullMask, incl, o);
+                        if (lane >= o) incl += v;
                     }
-                    if (j < n_slot) issue_pv(slot, j);
-                    if (!ok) break;
-                    if (last) umma_commit(empty(v_stage));
+                    const uint32_t hit = __ballot_sync(kFullMask, w < at + incl);
+                    if (hit) {
+                        const int l = __ffs(hit) - 1;
+                        b = b0 + l;
+                        at += __shfl_sync(kFullMask, incl - mine, l);
+                        break;
+                    }
+                    at += __shfl_sync(kFullMask, incl, 31);
+                    b = min(b0 + 32, p.batch);
                 }
-                if (i + 2 < steps) {
-                    if (first) acquire(k_stage);
-                    if (!ok) break;
-                    if (j + 1 < n_slot) issue_s(slot);
-                    if (last) umma_commit(empty(k_stage));
+                for (bool head = true; ok && w < w1 && b < p.batch; ++b) {
+                    const Seq q = load_seq(p, b);
+                    const int items = items_of(p, q.kept);
+                    for (int i = 0; i < items && ok && w < w1; ++i) {
+                        const int tiles = item_tiles(p, q, i);
+                        if (w >= at + (long long)tiles * p.Hkv) {
+                            at += (long long)tiles * p.Hkv;
+                            continue;
+                        }
+                        for (int g = (int)((w - at) / max(tiles, 1)); g < p.Hkv && ok && w < w1; ++g) {
+                            const long long a = at + (long long)g * tiles;
+                            const int first = (int)(w - a), last = (int)min((long long)tiles, w1 - a);
+                            const bool whole = first == 0 && last == tiles;
+                            emit(q, i, g, first, last, whole ? -1 : 2 * cta + (head ? 0 : 1));
+                            if (head && first > 0 && last == tiles) {
+                                // this item began in an earlier CTA and ends here
+                                int c0 = (int)(a * ctas / total);
+                                while (share_begin(total, c0 + 1, ctas) <= a) ++c0;
+                                while (share_begin(total, c0, ctas) > a) --c0;
+                                join_from = 2 * c0 + (share_begin(total, c0, ctas) == a ? 0 : 1);
+                                const int tok0 = i * 2 * tps;
+                                join_tok = q.begin + tok0;
+                                join_head = g << p.g_shift;
+                                join_rows = min(2 * tps, q.kept - tok0) << p.g_shift;
+                            }
+                            head = false;
+                            w = a + last;
+                        }
+                        at += (long long)tiles * p.Hkv;
+                    }
+                }
+                if (cta == 0) {  // the lengths' report, and items without a tile, which are in nobody's share
+                    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+                        bool odd = false;
+                        if (b0 + lane < p.batch) {
+                            const Seq q = load_seq(p, b0 + lane);
+                            const int t = q.n > 0 ? p.ctx_len[q.b] : 1;
+                            odd = t < 1 || t > p.cap || (q.n > 0 && q.n > q.T) || q.n > p.max_new;
+                        }
+                        for (uint32_t hits = __ballot_sync(kFullMask, odd); hits; hits &= hits - 1) {
+                            const Seq q = load_seq(p, b0 + __ffs(hits) - 1);
+                            report(q);
+                            for (int i = 0; i < items_of(p, q.kept) && item_tiles(p, q, i) == 0; ++i)
+                                for (int g = 0; g < p.Hkv; ++g) zero_item(q, i, g);
+                        }
+                    }
+                }
+                if (lane == 0) {
+                    int32_t *e = p.joins + 4 * cta;
+                    e[0] = join_from;
+                    e[1] = join_tok;
+                    e[2] = join_head;
+                    e[3] = join_rows;
                 }
             }
-            umma_commit(drain);  // no product is in flight when the CTA ends
-            mbar_wait_bounded(drain, 0, p.flags);
-        }
-        __syncwarp();
+            if (ok && k >= 2) ok = wait_warp(seg_empty(k & 1), ((k >> 1) + 1) & 1, abort_flag, p.flags);
+            if (ok && lane == 0) {
+                seg(k & 1)[kEnd] = 1;
+                mbar_arrive(seg_full(k & 1));
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ======================================================== loads
+            // Ring order = the order in which the products use the tiles: in
+            // pairs K0 V0 K1 V1 ..; else K0 K1 V0 K2 V1 .. V(n-2) V(n-1).
+            int stage = 0, issued = 0, tails = 0, queries = 0, k = 0;
+            uint32_t parity = 1;  // of a stage's previous release (passes at once in the first round)
+            bool ok = true;
+            for (;; ++k) {
+                ok = wait_warp(seg_full(k & 1), (k >> 1) & 1, abort_flag, p.flags);
+                if (!ok) break;
+                volatile const int *f = seg(k & 1);
+                if (f[kEnd]) break;
+                const bool pair = f[kPair];
+                const int nt = f[kTiles], row0 = f[kRowBase] + f[kFirst] * kTile, tail = f[kTail];
+                if (k > 0) ok = wait_warp(q_empty, (k - 1) & 1, abort_flag, p.flags);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int qn = pair ? 2 : 1, tok = f[kTok], head = f[kHead];
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(qn * L::kOperand));
+                    for (int s = 0; s < qn; ++s)
+#pragma unroll
+                        for (int a = 0; a < L::kAtoms; ++a)
+                            tma_load_3d(sb + s * L::kOperand + a * 16384, &tmQ, q_full, a * 64, head, tok + s * tps);
+                }
+                ++queries;
+                auto load = [&](bool is_k, int tile) {
+                    if (!ok) return;
+                    ok = wait_warp(empty(stage), parity, abort_flag, p.flags);
+                    if (!ok) return;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(full(stage), L::kOperand);
+#pragma unroll
+                        for (int a = 0; a < L::kAtoms; ++a)
+                            tma_load_2d(sb + L::kRing + stage * L::kOperand + a * 16384, is_k ? &tmK : &tmV, full(stage),
+                                        a * 64, row0 + tile * kTile);
+                    }
+                    ++issued;
+                    if (++stage == L::kStages) {
+                        stage = 0;
+                        parity ^= 1u;
+                    }
+                };
+                if (pair) {
+                    for (int t = 0; t < nt && ok; ++t) {
+                        load(true, t);
+                        load(false, t);
+                    }
+                } else {
+                    if (nt > 0) load(true, 0);
+                    if (nt > 1) load(true, 1);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        load(false, t);
+                        if (t + 2 < nt) load(true, t + 2);
+                    }
+                }
+                if (!ok) break;
+                if (tail > 0) {
+                    // the last V tile (the item just loaded) reaches past the
+                    // length: cache rows there may hold anything, NaN included,
+                    // and 0 * NaN must not reach the sums
+                    const int s = stage == 0 ? L::kStages - 1 : stage - 1;
+                    ok = wait_warp(full(s), ((issued - 1) / L::kStages) & 1, abort_flag, p.flags);
+                    if (!ok) break;
+                    uint8_t *v = sm + L::kRing + s * L::kOperand;
+#pragma unroll
+                    for (int a = 0; a < L::kAtoms; ++a)
+                        for (int o = tail * 128 + lane * 16; o < kTile * 128; o += 512)
+                            *reinterpret_cast<uint4 *>(v + a * 16384 + o) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    // (two barriers in turn: this warp may be a segment ahead of the products)
+                    if (lane == 0) mbar_arrive(tail_done(tails & 1));
+                    ++tails;
+                }
+                if (lane == 0) mbar_arrive(seg_empty(k & 1));
+                __syncwarp();
+            }
+            // leave only when every copy has landed
+            if (queries > 0) mbar_wait_bounded(q_full, (queries - 1) & 1, p.flags);
+            for (int i = max(0, issued - L::kStages); i < issued; ++i)
+                mbar_wait_bounded(full(i % L::kStages), (i / L::kStages) & 1, p.flags);
+        } else if (warp == 8) {
+            // ======================================================== products
+            // One thread issues all of them.  Per slot the order is S(0), then
+            // PV(j) S(j+1): S(j+1) overwrites the columns of P(j), which PV(j)
+            // has read by then (the products of one thread run in order).  PV
+            // is issued in two halves of 64 keys, so that its first half runs
+            // while the softmax works out the second half of the weights.
+            if (elect_one()) {
+                constexpr uint32_t id_s = idesc_bf16_f32(128, kTile);
+                constexpr uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
+                constexpr uint32_t kStep = L::kOperand >> 4;
+                const uint64_t kd = sw128_kmajor_desc(sb), vd = sw128_mnmajor_desc(sb + L::kRing, 16384);
+                const uint32_t q_lo = (uint32_t)kd, hi = (uint32_t)(kd >> 32);
+                const uint32_t k_lo = q_lo + (L::kRing >> 4), v_lo = (uint32_t)vd;
+                int k_stage = 0, v_stage = 0, next = 0;
+                uint32_t next_parity = 0, tails = 0, done = 0;  // done: bit s = parity of slot s's tiles so far
+                bool ok = true;
+                auto acquire = [&](int &st) {
+                    st = next;
+                    if (ok) ok = wait_role(full(next), next_parity, abort_flag, p.flags);
+                    if (++next == L::kStages) {
+                        next = 0;
+                        next_parity ^= 1u;
+                    }
+                };
+                for (int k = 0; ok; ++k) {
+                    ok = wait_role(seg_full(k & 1), (k >> 1) & 1, abort_flag, p.flags);
+                    if (!ok) break;
+                    volatile const int *f = seg(k & 1);
+                    if (f[kEnd]) break;
+                    const bool pair = f[kPair];
+                    const int nt = f[kTiles], nt0 = f[kTiles0], nt1 = f[kTiles1], tail = f[kTail];
+                    ok = wait_role(q_full, k & 1, abort_flag, p.flags);
+                    // step i belongs to slot i & 1; in pairs steps 2t and 2t+1
+                    // use tile t, else step i uses tile i.  Each round: the
+                    // step's PV, then the same slot's next S.
+                    const int steps = pair ? 2 * nt : nt;
+#pragma unroll 1
+                    for (int i = -2; i < steps && ok; ++i) {
+                        const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
+                        const bool first = !pair || slot == 0, last = !pair || slot == 1;
+                        if (i >= 0) {
+                            if (first) {
+                                acquire(v_stage);
+                                if (tail > 0 && (pair ? j : i) + 1 == nt && ok) {
+                                    ok = wait_role(tail_done(tails & 1), (tails >> 1) & 1u, abort_flag, p.flags);
+                                    ++tails;
+                                }
+                                // the previous segment's sums have been read
+                                if (i == 0 && k > 0 && ok) ok = wait_role(o_free, (k - 1) & 1, abort_flag, p.flags);
+                            }
+                            if (j < n_slot) {
+                                const uint32_t v = v_lo + v_stage * kStep;
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    if (ok) ok = wait_role(p_full(slot, half), (done >> slot) & 1u, abort_flag, p.flags);
+                                    if (!ok) break;
+                                    tc_fence_after();
+#pragma unroll
+                                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                                        umma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, v + kk * 128, hi,
+                                                id_o, (j | kk) ? 1u : 0u);
+                                }
+                                if (!ok) break;
+                                umma_commit(o_done(slot));
+                                done ^= 1u << slot;
+                            }
+                            if (!ok) break;
+                            if (last) umma_commit(empty(v_stage));
+                        }
+                        if (i + 2 < steps) {
+                            if (first) acquire(k_stage);
+                            if (!ok) break;
+                            if (j + 1 < n_slot) {
+                                tc_fence_after();
+                                const uint32_t q = q_lo + (pair ? slot : 0) * kStep, kl = k_lo + k_stage * kStep;
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint32_t o = (uint32_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+                                    umma_ss(tmem + slot * 128, q + o, kl + o, hi, id_s, kk > 0);
+                                }
+                                umma_commit(s_full(slot));
+                            }
+                            if (last) umma_commit(empty(k_stage));
+                            if (i + 3 == steps) umma_commit(q_empty);  // the segment's last S
+                        }
+                    }
+                    if (!ok) break;
+                    mbar_arrive(seg_empty(k & 1));
+                }
+                umma_commit(drain);  // no product is in flight when the CTA ends
+                mbar_wait_bounded(drain, 0, p.flags);
+            }
+            __syncwarp();
         }
     } else {
         // ============================================================ softmax
@@ -545,219 +769,238 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int slot = warp >> 2;
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_base + slot * 128, to = tmem + lane_base + 256 + slot * 128;
-        // this thread's row: token (within the sequence) and its last visible row
-        const int tok = it.tok0 + ((pair ? slot : 0) * tps) + (row >> p.g_shift);
-        const bool live = tok < it.tok0 + it.ntok;
-        const int base = it.T - it.n;  // first row of the new tokens
-        // the row sees every cache row below all_end, and of the drafted rows
-        // from all_end to draft_end those with a bit in mrow
-        const uint32_t *mrow = p.mask && live ? p.mask + (size_t)(it.begin + tok) * p.mask_words : nullptr;
-        const int all_end = !live ? 0 : p.mask ? base : base + tok + 1;
-        const int draft_end = base + min(it.n, p.max_new);
-        const int n_mine = slot ? nt1 : nt0;
-        // tiles from `masked_from` on hold rows that some row of this slot does not see
-        const int masked_from = p.mask ? max(base, 0) / kTile
-                                       : max(0, base + it.tok0 + (pair ? slot : 0) * tps + 1) / kTile;
-        float m = -INFINITY, l = 0.f;
+        const uint32_t ts = tmem + lane_base + slot * 128, to = tmem + lane_base + 256;
+        uint32_t count = 0, merges = 0;  // tiles of this slot so far; merged segments so far
+        uint32_t other_count = 0;        // tiles of the other slot so far
         bool ok = true;
-
-        // which of the 32 cache rows from p0 on this row attends to
-        auto allowed = [&](int p0) -> uint32_t {
-            uint32_t d = bits_below(all_end - p0);
-            if (mrow) {
-                const int j0 = p0 - all_end;  // drafted token at p0
-                uint32_t x = 0u;
-                if (j0 >= 0) {
-                    const int w = j0 >> 5, sh = j0 & 31;
-                    if (w < p.mask_words) x = __ldg(mrow + w) >> sh;
-                    if (sh && w + 1 < p.mask_words) x |= __ldg(mrow + w + 1) << (32 - sh);
-                } else if (j0 > -32) {
-                    x = __ldg(mrow) << -j0;
-                }
-                d |= x & bits_below(draft_end - p0);
-            }
-            return d;
-        };
-
-        for (int j = 0; j < n_mine; ++j) {
-            const int tile = t_first + (pair ? j : 2 * j + slot);
-            const bool masked = tile >= masked_from;
-            uint32_t see[4];
-            if (masked) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) see[q] = allowed(tile * kTile + q * 32);
-            }
-            ok = wait_warp(s_full(slot), j & 1, abort_flag, p.flags);
+        for (int k = 0; ok; ++k) {
+            ok = wait_warp(seg_full(k & 1), (k >> 1) & 1, abort_flag, p.flags);
             if (!ok) break;
-            tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_wait32(s[q]);
-            if (masked) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((see[q] >> k) & 1u)) s[q][k] = 0xff800000u;  // -inf
-            }
-            float mx[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = max3_nan(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
-#pragma unroll
-            for (int k = 3; k < 31; k += 2)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    mx[q] = max3_nan(mx[q], __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = max3_nan(mx[q], __uint_as_float(s[q][31]), mx[q]);
-            float top = max3_nan(mx[0], mx[1], max3_nan(mx[2], mx[3], mx[3])) * p.c;
-            // a NaN or +inf logit makes the row's softmax NaN: so becomes m, and l with it
-            if (!(top < INFINITY)) top = NAN;
-            const bool raise = !(top <= m + kLazy);  // also the first logit of a row (m = -inf)
-            if (__any_sync(kFullMask, raise)) {
-                const float m_new = raise ? top : m;
-                const float f = m_new == m ? 1.f : ex2(m - m_new);  // (-inf stays -inf while nothing is seen)
-                if (j > 0) {
-                    ok = wait_warp(o_done(slot), (j - 1) & 1, abort_flag, p.flags);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {  // rare: kept small, the logits fill the registers
-                        float o[16];
-                        uint32_t w[16];
-                        tmem_ld16(to + q * 16, o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * f);
-                        tmem_st16(to + q * 16, w);
-                    }
+            volatile const int *f = seg(k & 1);
+            if (f[kEnd]) break;
+            const bool pair = f[kPair];
+            const int t_step = pair ? 1 : 2, n_mine = slot ? f[kTiles1] : f[kTiles0];
+            const int p_step = t_step * kTile;
+            int p0 = (f[kFirst] + (pair ? 0 : slot)) * kTile;  // the tile's first cache row
+            // the row sees every cache row below all_end, and of the drafted
+            // rows from all_end to draft_end those with a bit in mrow
+            const uint32_t *mrow = nullptr;
+            int all_end = 0, draft_end = 0, masked_from;
+            {
+                const int ti = (pair ? slot * tps : 0) + (row >> p.g_shift);  // token of the item
+                const int base = f[kBase];
+                if (ti < f[kNTok]) {
+                    all_end = p.mask ? base : base + f[kTok0] + ti + 1;
+                    draft_end = f[kDraftEnd];
+                    if (p.mask) mrow = p.mask + (size_t)(f[kTok] + ti) * p.mask_words;
                 }
-                l *= f;
-                m = m_new;
+                // tiles that reach past this cache row hold rows that some row of this slot does not see
+                masked_from = p.mask ? base : base + f[kTok0] + (pair ? slot * tps : 0) + 1;
             }
-            const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: 2^(-inf - 0) = 0
-            const uint64_t c2 = pack2(p.c, p.c), nm2 = pack2(-mm, -mm);
-            uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const uint64_t x2 = fma2(pack2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), c2, nm2);
-                    float e0, e1;
-                    if ((k & 7) < kPolyOf8) {
-                        ex2_poly2(x2, e0, e1);
-                    } else {
-                        unpack2(x2, e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                    }
-                    sum2[k & 1] = add2(sum2[k & 1], pack2(e0, e1));
-                    // rounded to bf16 for the second product: 2^-9 relative per
-                    // weight, below the rounding of the bf16 result
-                    w[k] = pack_bf16(e0, e1);
-                }
-                tmem_st16(ts + q * 16, w);
-                if (q & 1) {  // half of the weights are in place
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full(slot, q >> 1));
-                }
-            }
-            float u0, u1;
-            unpack2(add2(sum2[0], sum2[1]), u0, u1);
-            l += u0 + u1;
-        }
+            float m = -INFINITY, l = 0.f;
 
-        // ---- epilogue
-        if (ok && n_mine > 0) ok = wait_warp(o_done(slot), (n_mine - 1) & 1, abort_flag, p.flags);
-        if (!pair && ok) {  // both slots' products are done before the ring's memory is reused
-            const int other = slot ? nt0 : nt1;
-            if (other > 0) ok = wait_warp(o_done(slot ^ 1), (other - 1) & 1, abort_flag, p.flags);
-        }
-        tc_fence_after();
-        float *xch = reinterpret_cast<float *>(sm + L::kRing);  // [D + 2][128]: slot 1's state
-        if (!pair && nt1 > 0) {
-            if (slot == 1) {
-                if (ok) {
-#pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(to + q * 32, o);
-                        tmem_wait32(o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) xch[(q * 32 + k) * 128 + row] = __uint_as_float(o[k]);
+            // which of the 32 cache rows from r on this row attends to
+            auto allowed = [&](int r) -> uint32_t {
+                uint32_t d = bits_below(all_end - r);
+                if (mrow) {
+                    const int j0 = r - all_end;  // drafted token at r
+                    uint32_t x = 0u;
+                    if (j0 >= 0) {
+                        const int w = j0 >> 5, sh = j0 & 31;
+                        if (w < p.mask_words) x = __ldg(mrow + w) >> sh;
+                        if (sh && w + 1 < p.mask_words) x |= __ldg(mrow + w + 1) << (32 - sh);
+                    } else if (j0 > -32) {
+                        x = __ldg(mrow) << -j0;
                     }
-                    xch[D * 128 + row] = m;
-                    xch[(D + 1) * 128 + row] = l;
+                    d |= x & bits_below(draft_end - r);
                 }
+                return d;
+            };
+
+            for (int j = 0; j < n_mine; ++j, p0 += p_step, ++count) {
+                const bool masked = p0 + kTile > masked_from;
+                uint32_t see[4];
+                if (masked) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) see[q] = allowed(p0 + q * 32);
+                }
+                ok = wait_warp(s_full(slot), count & 1, abort_flag, p.flags);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_wait32(s[q]);
+                if (masked) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see[q] >> i) & 1u)) s[q][i] = 0xff800000u;  // -inf
+                }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mx[q] = max3_nan(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
+#pragma unroll
+                for (int i = 3; i < 31; i += 2)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = max3_nan(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mx[q] = max3_nan(mx[q], __uint_as_float(s[q][31]), mx[q]);
+                float top = max3_nan(mx[0], mx[1], max3_nan(mx[2], mx[3], mx[3])) * p.c;
+                // a NaN or +inf logit makes the row's softmax NaN: so becomes m, and l with it
+                if (!(top < INFINITY)) top = NAN;
+                const bool raise = !(top <= m + kLazy);  // also the first logit of a row (m = -inf)
+                if (__any_sync(kFullMask, raise)) {
+                    const float m_new = raise ? top : m;
+                    const float fac = m_new == m ? 1.f : ex2(m - m_new);  // (-inf stays -inf while nothing is seen)
+                    if (j > 0) {
+                        ok = wait_warp(o_done(slot), (count - 1) & 1, abort_flag, p.flags);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {  // rare: kept small, the logits fill the registers
+                            float o[16];
+                            uint32_t w[16];
+                            tmem_ld16(to + slot * 128 + q * 16, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * fac);
+                            tmem_st16(to + slot * 128 + q * 16, w);
+                        }
+                    }
+                    l *= fac;
+                    m = m_new;
+                }
+                const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: 2^(-inf - 0) = 0
+                const uint64_t c2 = pack2(p.c, p.c), nm2 = pack2(-mm, -mm);
+                uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t x2 =
+                            fma2(pack2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
+                        float e0, e1;
+                        if ((i & 7) < kPolyOf8) {
+                            ex2_poly2(x2, e0, e1);
+                        } else {
+                            unpack2(x2, e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                        }
+                        sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
+                        // rounded to bf16 for the second product: 2^-9 relative
+                        // per weight, below the rounding of the bf16 result
+                        w[i] = pack_bf16(e0, e1);
+                    }
+                    tmem_st16(ts + q * 16, w);
+                    if (q & 1) {  // half of the weights are in place
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full(slot, q >> 1));
+                    }
+                }
+                float u0, u1;
+                unpack2(add2(sum2[0], sum2[1]), u0, u1);
+                l += u0 + u1;
             }
-            bar_named(kBarMerge, 256);
-        }
-        if (ok && (pair || slot == 0)) {
-            float f0 = 1.f, f1 = 0.f;
-            const bool two = !pair && nt1 > 0;
-            if (two) {
-                const float m1 = xch[D * 128 + row], l1 = xch[(D + 1) * 128 + row];
+            if (!ok) break;
+
+            // ---- epilogue: in pairs each slot its own rows; else both slots
+            // the same rows, each half of the head dims of the merged sums
+            const int n_other = slot ? f[kTiles0] : f[kTiles1];
+            if (n_mine > 0) ok = wait_warp(o_done(slot), (count - 1) & 1, abort_flag, p.flags);
+            if (!ok) break;
+            float f0 = 1.f, f1 = 0.f;  // this slot's and the other's factor
+            if (!pair) {
+                volatile float *st = reinterpret_cast<volatile float *>(sm + L::kState);
+                if (merges > 0) ok = wait_warp(state_empty, (merges - 1) & 1, abort_flag, p.flags);
+                if (!ok) break;
+                st[slot * 256 + row] = m;
+                st[slot * 256 + 128 + row] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(state_full);
+                ok = wait_warp(state_full, merges & 1, abort_flag, p.flags);
+                if (ok && n_other > 0)
+                    ok = wait_warp(o_done(slot ^ 1), (other_count + n_other - 1) & 1, abort_flag, p.flags);
+                if (!ok) break;
+                ++merges;
+                const float m1 = st[(slot ^ 1) * 256 + row], l1 = st[(slot ^ 1) * 256 + 128 + row];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(state_empty);
+                // (a NaN m makes its factor NaN; both slots do the same arithmetic on (slot 0, slot 1))
                 const float mn = fmaxf(m, m1);
                 f0 = m == -INFINITY ? 0.f : ex2(m - mn);
                 f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mn);
-                l = l * f0 + l1 * f1;
+                l = slot ? fmaf(l1, f1, l * f0) : fmaf(l, f0, l1 * f1);
                 m = mn;
             }
-            const bool empty_row = !(l > 0.f) && !(l != l);  // attended to nothing: 0 (a NaN sum stays NaN)
-            if (p.splits == 1) {
+            other_count += n_other;
+            tc_fence_after();
+            const int part_slot = f[kPart];
+            const bool empty_row = l == 0.f;  // attended to nothing: 0 (a NaN sum stays NaN)
+            if (part_slot < 0) {
                 const float inv = empty_row ? 0.f : 1.f / l;
                 f0 *= inv;
                 f1 *= inv;
             }
-            const int h = (g << p.g_shift) + (row & ((1 << p.g_shift) - 1));
-            const int ti = (pair ? slot * tps : 0) + (row >> p.g_shift);  // token of the item
-            const bool store = ti < misc[3];
-            uint16_t *dst = p.out + ((size_t)(misc[2] + ti) * p.Hq + h) * D;
-            float *part = p.part ? p.part + (((size_t)misc[4] * p.Hkv + g) * p.splits + split) * ((D + 2) * kItemRows) +
-                                       (pair ? slot : 0) * kSlotRows + row
-                                 : nullptr;
+            const int ti = (pair ? slot * tps : 0) + (row >> p.g_shift);
+            const bool store = ti < f[kNTok];
+            const int h = f[kHead] + (row & ((1 << p.g_shift) - 1));
+            uint16_t *dst = p.out + ((size_t)(f[kTok] + ti) * p.Hq + h) * D;
+            float *part = p.part + (size_t)max(part_slot, 0) * ((D + 2) * kItemRows) + (pair ? slot : 0) * kSlotRows + row;
+            const int q0 = pair ? 0 : slot * (D / 32), q1 = pair ? D / 16 : q0 + D / 32;  // groups of 16 head dims
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                if (n_mine > 0) {
-                    tmem_ld32(to + q * 32, o);
-                    tmem_wait32(o);
-                } else {
+            for (int q = q0; q < q1; ++q) {
+                float o[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0u;
-                }
+                for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                if (n_mine > 0) tmem_ld16(to + slot * 128 + q * 16, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float v = __uint_as_float(o[k]) * f0;
-                    if (two) v = fmaf(xch[(q * 32 + k) * 128 + row], f1, v);
-                    o[k] = empty_row ? 0u : __float_as_uint(v);
+                for (int i = 0; i < 16; ++i) o[i] *= f0;
+                if (!pair && n_other > 0) {
+                    float o1[16];
+                    tmem_ld16(to + (slot ^ 1) * 128 + q * 16, o1);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = fmaf(o1[i], f1, o[i]);
                 }
-                if (p.splits == 1) {
+                if (q + 1 == q1) {  // the sums have been read: the next segment may overwrite them
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_free);
+                }
+                if (empty_row) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                }
+                if (part_slot < 0) {
                     if (store) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int i = 0; i < 2; ++i) {
                             uint4 w;
-                            w.x = pack_bf16(__uint_as_float(o[8 * k + 0]), __uint_as_float(o[8 * k + 1]));
-                            w.y = pack_bf16(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]));
-                            w.z = pack_bf16(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]));
-                            w.w = pack_bf16(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]));
-                            *reinterpret_cast<uint4 *>(dst + q * 32 + k * 8) = w;
+                            w.x = pack_bf16(o[8 * i + 0], o[8 * i + 1]);
+                            w.y = pack_bf16(o[8 * i + 2], o[8 * i + 3]);
+                            w.z = pack_bf16(o[8 * i + 4], o[8 * i + 5]);
+                            w.w = pack_bf16(o[8 * i + 6], o[8 * i + 7]);
+                            *reinterpret_cast<uint4 *>(dst + q * 16 + i * 8) = w;
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) part[(size_t)(q * 32 + k) * kItemRows] = __uint_as_float(o[k]);
+                    for (int i = 0; i < 16; ++i) part[(size_t)(q * 16 + i) * kItemRows] = o[i];
                 }
             }
-            if (p.splits > 1) {
+            if (part_slot >= 0 && (pair || slot == 0)) {
                 part[(size_t)D * kItemRows] = m;
                 part[(size_t)(D + 1) * kItemRows] = l;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_empty(k & 1));
         }
     }
     tc_fence_before();
@@ -766,56 +1009,82 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if (tid == 0 && p.part == nullptr) {
+        // the last CTA to finish leaves the counter as it was found
+        if (atom_add_acq_rel_gpu(p.counter + 1, 1u) == gridDim.x - 1) {
+            p.counter[0] = 0u;
+            p.counter[1] = 0u;
+        }
+    }
 }
 
-// Joins the splits' states: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-// One CTA: 32 rows of one item; warp w takes the head dims congruent to w
-// (lane = row, so the states are read 128 bytes at a time), then the tile is
-// turned in shared memory and stored row by row.
+// Joins the states of an item that was shared out:
+//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// blockIdx.x is the CTA in whose first segment the item ends (it says so in
+// its entry), y a block of 32 rows (lane = row, so the states are read 128
+// bytes at a time), z a block of 32 head dims, 8 per warp.  The tile is turned
+// in shared memory and stored row by row.
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 multi_join_kernel(const Params p) {
-    __shared__ float tile[32][D + 1];
+    __shared__ float tile[32][33];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    Item it = find_item(p, (int)blockIdx.x, lane);
-    if (!it.any) return;
-    const int g = blockIdx.y, row = blockIdx.z * 32 + lane;
-    const int rows = it.ntok << p.g_shift;
-    if ((int)blockIdx.z * 32 >= rows) return;
-    it.T = clamp_ctx(p.ctx_len[it.b], p.cap, nullptr, false);
-    const int tiles = tiles_upto(p, it, it.tok0 + it.ntok - 1);
-    const int per = (tiles + p.splits - 1) / p.splits;
-    const int used = per > 0 ? (tiles + per - 1) / per : 0;  // splits that had a tile
+    const int32_t *e = p.joins + 4 * blockIdx.x;
+    const int from = e[0], tok = e[1], head = e[2], rows = e[3];
+    if (from < 0 || (int)blockIdx.y * 32 >= rows) return;
+    const int n = (int)blockIdx.x - (from >> 1) + 1;  // CTAs from >> 1 .. blockIdx.x, the first one's state `from`
     constexpr size_t kRec = (size_t)(D + 2) * kItemRows;
-    const float *part = p.part + ((size_t)it.index * p.Hkv + g) * p.splits * kRec + row;
-    float M = -INFINITY;
-    for (int s = 0; s < used; ++s) M = fmaxf(M, part[s * kRec + (size_t)D * kItemRows]);
-    float acc[D / 8], l = 0.f;
+    const int d0 = blockIdx.z * 32 + warp * 8;
+    const float *base = p.part + blockIdx.y * 32 + lane;
+    float M = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k) acc[k] = 0.f;
-    for (int s = 0; s < used; ++s) {
-        const float *ps = part + s * kRec;
-        const float ms = ps[(size_t)D * kItemRows];
-        const float f = ms == -INFINITY ? 0.f : ex2(ms - M);
-        l = fmaf(ps[(size_t)(D + 1) * kItemRows], f, l);
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    constexpr int kBatch = 4;
+    for (int s0 = 0; s0 < n; s0 += kBatch) {
+        float ms[kBatch], ls[kBatch], v[kBatch][8];
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) acc[k] = fmaf(ps[(size_t)(k * 8 + warp) * kItemRows], f, acc[k]);
+        for (int u = 0; u < kBatch; ++u) {
+            ms[u] = -INFINITY;
+            ls[u] = 0.f;
+            if (s0 + u < n) {
+                const float *r = base + (size_t)(s0 + u ? 2 * ((from >> 1) + s0 + u) : from) * kRec;
+                ms[u] = r[(size_t)D * kItemRows];
+                ls[u] = r[(size_t)(D + 1) * kItemRows];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] = r[(size_t)(d0 + i) * kItemRows];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, ms[u]);
+        const float f = M == -INFINITY ? 0.f : ex2(M - mn);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] *= f;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const float fu = ms[u] == -INFINITY ? 0.f : ex2(ms[u] - mn);  // NaN stays NaN
+            l = fmaf(ls[u], fu, l);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[u][i], fu, acc[i]);
+        }
+        M = mn;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k) tile[lane][k * 8 + warp] = acc[k] * inv;
+    for (int i = 0; i < 8; ++i) tile[lane][warp * 8 + i] = acc[i] * inv;
     __syncthreads();
-    for (int e = tid; e < 32 * (D / 8); e += 256) {
-        const int r = e / (D / 8), c8 = e % (D / 8), rr = blockIdx.z * 32 + r;
-        if (rr >= rows) break;
-        const float *t = &tile[r][c8 * 8];
-        uint4 w = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]), pack_bf16(t[4], t[5]), pack_bf16(t[6], t[7]));
-        const int tok = it.begin + it.tok0 + (rr >> p.g_shift);
-        const int h = (g << p.g_shift) + (rr & ((1 << p.g_shift) - 1));
-        *reinterpret_cast<uint4 *>(p.out + ((size_t)tok * p.Hq + h) * D + c8 * 8) = w;
-    }
+    const int r = tid >> 2, c8 = (tid & 3) * 8, rr = blockIdx.y * 32 + r;
+    if (rr >= rows) return;
+    const float *t = &tile[r][c8];
+    const uint4 w = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]), pack_bf16(t[4], t[5]), pack_bf16(t[6], t[7]));
+    const size_t at = (size_t)(tok + (rr >> p.g_shift)) * p.Hq + head + (rr & ((1 << p.g_shift) - 1));
+    *reinterpret_cast<uint4 *>(p.out + at * D + blockIdx.z * 32 + c8) = w;
 }
 
 // ---------------------------------------------------------------- host side
@@ -861,24 +1130,18 @@ long long item_bound(const tb_dims &d, int32_t n_tokens, int32_t max_new) {
     return a < b ? a : b;
 }
 
-// Splits along the context: as many as fill the SMs in whole waves, counted
-// in tiles of the longest possible item, each split paying a few tiles' time
-// for its set-up, state and join.
-int pick_splits(const tb_dims &d, long long items) {
-    const long long ctas = items * d.n_kv_heads, sms = num_sms();
-    const long long tiles = (d.ctx_cap + kTile - 1) / kTile;
-    long long best = 0;
-    int best_s = 1;
-    for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-        const long long waves = (ctas * s + sms - 1) / sms;
-        const long long cost = waves * ((tiles + s - 1) / s + (s > 1 ? 8 : 2));
-        if (s == 1 || cost < best) {
-            best = cost;
-            best_s = s;
-        }
-        if (ctas * s > 4 * sms) break;
-    }
-    return best_s;
+// Deal whole items out by the counter, or equal shares of all tiles?  In tiles
+// of the longest context the cache holds (the lengths are the device's): whole
+// items take the average load and, at the end, about half of the smallest item
+// that may come last; at least one whole item.  Shares are even but write and
+// join states, about 8 tiles' time.
+bool use_shares(const tb_dims &d, int32_t max_new, bool tree, long long items) {
+    const double ctas = num_sms(), n = (double)items * d.n_kv_heads;
+    const double longest = (d.ctx_cap + kTile - 1) / kTile;
+    const double shortest = tree ? longest : fmax(1.0, (double)(d.ctx_cap - max_new) / kTile);
+    const double average = 0.5 * (longest + shortest);
+    const double whole = fmax(longest, n * average / ctas + 0.5 * shortest);
+    return n * average / ctas + 8.0 < whole;
 }
 
 template <int D>
@@ -896,31 +1159,33 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
     static std::atomic<int> smem_set[kMaxDevices];
     cudaError_t e = ensure_dynamic_smem((const void *)multi_attn_kernel<D>, L::kBytes, smem_set);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((long long)p.item_bound * p.Hkv * p.splits));
-    e = launch_pdl(multi_attn_kernel<D>, grid, dim3(kThreads), L::kBytes, st, mQ, mK, mV, p);
-    if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_pdl(multi_join_kernel<D>, dim3((unsigned)p.item_bound, (unsigned)p.Hkv, kItemRows / 32), dim3(256), 0,
-                      st, p);
+    const long long items = (long long)p.item_bound * p.Hkv, sms = num_sms();
+    const unsigned ctas = (unsigned)(p.part || items > sms ? sms : items);
+    e = launch_pdl(multi_attn_kernel<D>, dim3(ctas), dim3(kThreads), L::kBytes, st, mQ, mK, mV, p);
+    if (e != cudaSuccess || !p.part) return e;
+    return launch_pdl(multi_join_kernel<D>, dim3(ctas, kItemRows / 32, D / 32), dim3(128), 0, st, p);
 }
 
 }  // namespace
 
-size_t multi_attn_ws_bytes(const tb_dims &d, int32_t n_tokens, int32_t max_new) {
-    const long long items = item_bound(d, n_tokens, max_new);
-    const int s = pick_splits(d, items);
-    if (s == 1) return kWsHeaderBytes;
-    return kWsHeaderBytes + (size_t)items * d.n_kv_heads * s * (d.head_dim + 2) * kItemRows * sizeof(float);
+// Workspace: flag word, counter (at 64), the CTAs' join entries, their states.
+size_t multi_attn_ws_bytes(const tb_dims &d, int32_t n_tokens, int32_t max_new, bool tree) {
+    if (!use_shares(d, max_new, tree, item_bound(d, n_tokens, max_new))) return kWsHeaderBytes;
+    const size_t ctas = (size_t)num_sms();
+    return kWsHeaderBytes + align_up(ctas * 16, 256) + ctas * 2 * (d.head_dim + 2) * kItemRows * sizeof(float);
 }
 
 cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
                               const int32_t *q_begin, int32_t n_tokens, int32_t max_new, const int32_t *ctx_len,
                               const uint32_t *mask, float scale, uint16_t *out, void *ws, cudaStream_t st) {
     Params p{};
+    uint8_t *w = static_cast<uint8_t *>(ws);
     p.q_begin = q_begin;
     p.ctx_len = ctx_len;
     p.mask = mask;
     p.out = out;
-    p.flags = static_cast<uint32_t *>(ws);
+    p.flags = reinterpret_cast<uint32_t *>(w);
+    p.counter = reinterpret_cast<uint32_t *>(w + 64);
     p.batch = d.batch;
     p.Hq = d.n_q_heads;
     p.Hkv = d.n_kv_heads;
@@ -930,8 +1195,10 @@ cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_
     p.mask_words = (max_new + 31) / 32;
     p.g_shift = log2_int(d.n_q_heads / d.n_kv_heads);
     p.item_bound = (int)item_bound(d, n_tokens, max_new);
-    p.splits = pick_splits(d, p.item_bound);
-    p.part = p.splits > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kWsHeaderBytes) : nullptr;
+    if (use_shares(d, max_new, mask != nullptr, p.item_bound)) {
+        p.joins = reinterpret_cast<int32_t *>(w + kWsHeaderBytes);
+        p.part = reinterpret_cast<float *>(w + kWsHeaderBytes + align_up((size_t)num_sms() * 16, 256));
+    }
     p.c = scale * 1.4426950408889634f;
     return d.head_dim == 128 ? launch_d<128>(d, Q, K, V, p, st) : launch_d<64>(d, Q, K, V, p, st);
 }
