@@ -59,7 +59,7 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;               // log2 units
-constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
+constexpr int kPolyOf8 = 3;                 // of 8 pairs of weights, those worked out on the FMA pipe
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 template <int D>
@@ -70,7 +70,7 @@ struct Lay {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kOperand;
     static constexpr int kBar = kRing + kStages * kOperand;
-    static constexpr int kNumBars = 2 * kStages + 20;
+    static constexpr int kNumBars = 2 * kStages + 21;
     static constexpr int kMisc = kBar + kNumBars * 8;       // TMEM base, abort flag
     static constexpr int kSeg = (kMisc + 8 + 15) / 16 * 16; // two segment descriptions
     static constexpr int kState = kSeg + 2 * 64;            // the slots' m and l [2 slots][2][128]
@@ -386,6 +386,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     auto s_full = [&](int s) { return bar(kB + 11 + s); };
     auto p_full = [&](int s, int half) { return bar(kB + 13 + 2 * s + half); };  // keys 0..63, 64..127
     auto o_done = [&](int s) { return bar(kB + 17 + s); };
+    const uint32_t loaded = bar(kB + 20);
     auto tail_done = [&](int i) { return bar(i ? kB + 19 : kB + 2); };
     auto seg = [&](int i) { return reinterpret_cast<volatile int *>(sm + L::kSeg + i * 64); };
 
@@ -398,6 +399,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(drain, 1);
+        mbar_init(loaded, 1);
         mbar_init(o_free, 8);
         mbar_init(state_full, 8);
         mbar_init(state_empty, 8);
@@ -481,6 +483,11 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (p.part == nullptr) {
                 // from the last item to the first: a sequence's last tokens have the most tiles
                 while (ok) {
+                    // the next item is taken when the current one's last tiles
+                    // are on their way: early enough to overlap, and no CTA
+                    // holds a second long item while others run dry
+                    if (k > 0) ok = wait_warp(loaded, (k - 1) & 1, abort_flag, p.flags);
+                    if (!ok) break;
                     int next = 0;
                     if (lane == 0) next = (int)atomicAdd(p.counter, 1u);
                     next = __shfl_sync(kFullMask, next, 0);
@@ -661,7 +668,10 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (lane == 0) mbar_arrive(tail_done(tails & 1));
                     ++tails;
                 }
-                if (lane == 0) mbar_arrive(seg_empty(k & 1));
+                if (lane == 0) {
+                    mbar_arrive(loaded);
+                    mbar_arrive(seg_empty(k & 1));
+                }
                 __syncwarp();
             }
             // leave only when every copy has landed
