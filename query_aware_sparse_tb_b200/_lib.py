@@ -330,41 +330,49 @@ def kv_append(d: TbDims, n_layers: int, src, caches, ctx_len, ws, stream=None):
 
 
 # The calls that take several new tokens of a sequence at once check what the C
-# side cannot see: types, shapes against dims, and that every tensor is on one
-# device, which is made current for the call (the default stream is that
-# device's current one).
+# side cannot see: types, shapes against dims, and that every tensor is on the
+# workspace's device, which is made current for the call (without a stream
+# argument they run on that device's current stream).  They are called once per
+# layer of a step of a few microseconds, so the checks are kept to plain
+# comparisons and the message is put together only once one has failed.
 
-def _tensor(name, t, dtype, shape, device):
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def _misfit(name, t, dtype, shape, dev):
+    """Raise for the first thing wrong with tensor `t` (there is one)."""
     if not t.is_cuda:
         raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes device tensors")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype:
         raise TbError(TB_ERR_INVALID_ARG, f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise TbError(TB_ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes contiguous tensors")
-    if t.device != device:
-        raise TbError(TB_ERR_INVALID_ARG, f"{name} is on {t.device}, the workspace on {device}")
+    if t.shape != shape:
+        raise TbError(TB_ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != dev:
+        raise TbError(TB_ERR_INVALID_ARG, f"{name} is on {t.device}, the workspace on cuda:{dev}")
+    raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes contiguous tensors")
 
 
-def _device_of(ws):
-    if not ws.is_cuda:
-        raise TbError(TB_ERR_INVALID_ARG, "ws: libtb takes device tensors")
-    return ws.device
+def _at(name, t, dtype, shape, dev):
+    """Address of a contiguous device tensor of that type and shape."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous() or dev < 0:
+        _misfit(name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-_WORDS = (torch.int32, torch.uint32)
+def _call_on(dev: int, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, *args)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st != TB_OK:
+        _check(st)
 
 
-def _check_multi(d: TbDims, Q, K, V, q_begin, ctx_len, ws):
-    dev = _device_of(ws)
-    bf = torch.bfloat16
-    _tensor("Q", Q, bf, (Q.shape[0], d.n_q_heads, d.head_dim), dev)
-    for name, t in (("K", K), ("V", V)):
-        _tensor(name, t, bf, (d.batch, d.n_kv_heads, d.ctx_cap, d.head_dim), dev)
-    _tensor("q_begin", q_begin, torch.int32, (d.batch + 1,), dev)
-    _tensor("ctx_len", ctx_len, torch.int32, (d.batch,), dev)
-    return dev
+def _host_only(*tensors):
+    for t in tensors:
+        if not t.is_cuda:
+            raise TbError(TB_ERR_INVALID_ARG, "libtb takes device tensors")
 
 
 def norm_rope_append(d: TbDims, qkv, q_begin, ctx_len, pos, q_weight, k_weight, eps: float, inv_freq,
@@ -373,26 +381,34 @@ def norm_rope_append(d: TbDims, qkv, q_begin, ctx_len, pos, q_weight, k_weight, 
     further apart); pos [n_tokens] int32 or None (the cache row); q_weight and
     k_weight [d] bf16 or None; inv_freq [rot_dim / 2] float64 or None; writes Q
     [n_tokens][Hq][d] and the new rows of the caches K and V."""
-    dev = _check_multi(d, Q, K, V, q_begin, ctx_len, ws)
-    n, width = Q.shape[0], (d.n_q_heads + 2 * d.n_kv_heads) * d.head_dim
-    if not qkv.is_cuda or qkv.device != dev or qkv.dtype != torch.bfloat16 or tuple(qkv.shape) != (n, width) or \
-            qkv.stride(1) != 1:
-        raise TbError(TB_ERR_INVALID_ARG, f"qkv: expected bfloat16 [{n}][{width}] on {dev} with contiguous rows")
-    if pos is not None:
-        _tensor("pos", pos, torch.int32, (n,), dev)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _tensor(name, t, torch.bfloat16, (d.head_dim,), dev)
-    rot = 0
-    if inv_freq is not None:
-        _tensor("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
-        rot = 2 * inv_freq.numel()
-    stride = qkv.stride(0) if n > 1 else max(width, qkv.stride(0))
-    with torch.cuda.device(dev):
-        _check(load().tb_norm_rope_append(ctypes.byref(d), qkv.data_ptr(), stride, _ptr(q_begin), n, _ptr(ctx_len),
-                                          _ptr(pos), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), rot,
-                                          TB_ROPE_INTERLEAVED if interleaved else TB_ROPE_HALF, _ptr(Q), _ptr(K),
-                                          _ptr(V), _ptr(ws), _bytes(ws), _stream(stream)))
+    dev, B, hq, hkv, hd = ws.get_device(), d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim
+    n, width, cache = Q.shape[0], (hq + 2 * hkv) * hd, (B, hkv, d.ctx_cap, hd)
+    stride, inner = qkv.stride() if qkv.dim() == 2 else (0, 0)
+    if dev < 0 or qkv.get_device() != dev or qkv.dtype is not _BF16 or qkv.shape != (n, width) or inner != 1:
+        _host_only(ws, qkv)
+        raise TbError(TB_ERR_INVALID_ARG, f"qkv: expected bfloat16 [{n}][{width}] on cuda:{dev} with contiguous rows")
+    _call_on(dev, stream, (_lib or load()).tb_norm_rope_append, ctypes.byref(d), qkv.data_ptr(),
+             stride if n > 1 else max(width, stride), _at("q_begin", q_begin, _I32, (B + 1,), dev), n,
+             _at("ctx_len", ctx_len, _I32, (B,), dev), None if pos is None else _at("pos", pos, _I32, (n,), dev),
+             None if q_weight is None else _at("q_weight", q_weight, _BF16, (hd,), dev),
+             None if k_weight is None else _at("k_weight", k_weight, _BF16, (hd,), dev), eps,
+             None if inv_freq is None else _at("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev),
+             0 if inv_freq is None else 2 * inv_freq.numel(), TB_ROPE_INTERLEAVED if interleaved else TB_ROPE_HALF,
+             _at("Q", Q, _BF16, (n, hq, hd), dev), _at("K", K, _BF16, cache, dev), _at("V", V, _BF16, cache, dev),
+             ws.data_ptr(), ws.nbytes)
+
+
+def _multi_attn(fn, d: TbDims, Q, K, V, q_begin, max_new, ctx_len, mask, scale, out, ws, stream):
+    dev, B, hq, hd = ws.get_device(), d.batch, d.n_q_heads, d.head_dim
+    n = Q.shape[0]
+    rows, cache = (n, hq, hd), (B, d.n_kv_heads, d.ctx_cap, hd)
+    args = (ctypes.byref(d), _at("Q", Q, _BF16, rows, dev), _at("K", K, _BF16, cache, dev),
+            _at("V", V, _BF16, cache, dev), _at("q_begin", q_begin, _I32, (B + 1,), dev), n, max_new,
+            _at("ctx_len", ctx_len, _I32, (B,), dev))
+    if mask is not None:
+        words = mask.dtype if mask.dtype is torch.uint32 else _I32
+        args += (_at("mask", mask, words, (n, (max_new + 31) // 32), dev),)
+    _call_on(dev, stream, fn, *args, scale, _at("out", out, _BF16, rows, dev), ws.data_ptr(), ws.nbytes)
 
 
 def prompt_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
@@ -403,12 +419,7 @@ def prompt_attn(d: TbDims, Q, K, V, q_begin, max_new: int, ctx_len, scale: float
     """tb_prompt_attn: causal attention of packed prompts over the caches;
     Q and out [n_tokens][Hq][d] bf16, q_begin [batch + 1] int32, max_new an
     upper bound on a sequence's new tokens."""
-    dev = _check_multi(d, Q, K, V, q_begin, ctx_len, ws)
-    _tensor("out", out, torch.bfloat16, Q.shape, dev)
-    with torch.cuda.device(dev):
-        _check(load().tb_prompt_attn(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(q_begin), Q.shape[0],
-                                     int(max_new), _ptr(ctx_len), float(scale), _ptr(out), _ptr(ws), _bytes(ws),
-                                     _stream(stream)))
+    _multi_attn((_lib or load()).tb_prompt_attn, d, Q, K, V, q_begin, max_new, ctx_len, None, scale, out, ws, stream)
 
 
 def tree_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
@@ -418,28 +429,20 @@ def tree_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
 def tree_attn(d: TbDims, Q, K, V, q_begin, max_new: int, ctx_len, mask, scale: float, out, ws, stream=None):
     """tb_tree_attn: as prompt_attn, with the drafted tokens' attention bits
     mask [n_tokens][ceil(max_new / 32)] (int32 or uint32 words)."""
-    dev = _check_multi(d, Q, K, V, q_begin, ctx_len, ws)
-    _tensor("out", out, torch.bfloat16, Q.shape, dev)
-    _tensor("mask", mask, _WORDS, (Q.shape[0], (int(max_new) + 31) // 32), dev)
-    with torch.cuda.device(dev):
-        _check(load().tb_tree_attn(ctypes.byref(d), _ptr(Q), _ptr(K), _ptr(V), _ptr(q_begin), Q.shape[0],
-                                   int(max_new), _ptr(ctx_len), _ptr(mask), float(scale), _ptr(out), _ptr(ws),
-                                   _bytes(ws), _stream(stream)))
+    if mask is None:
+        raise TbError(TB_ERR_INVALID_ARG, "tree_attn needs a mask")
+    _multi_attn((_lib or load()).tb_tree_attn, d, Q, K, V, q_begin, max_new, ctx_len, mask, scale, out, ws, stream)
 
 
 def tree_accept(d: TbDims, n_layers: int, caches, q_begin, ctx_len, path, path_len, new_len, ws, stream=None):
     """tb_tree_accept: caches as for kv_append; path [batch][path_cap] int32,
     path_len and new_len [batch] int32."""
-    dev = _device_of(ws)
-    _tensor("caches", caches, torch.int64, (2 * int(n_layers),), dev)
-    _tensor("q_begin", q_begin, torch.int32, (d.batch + 1,), dev)
-    _tensor("path", path, torch.int32, (d.batch, path.shape[-1]), dev)
-    for name, t in (("ctx_len", ctx_len), ("path_len", path_len), ("new_len", new_len)):
-        _tensor(name, t, torch.int32, (d.batch,), dev)
-    with torch.cuda.device(dev):
-        _check(load().tb_tree_accept(ctypes.byref(d), int(n_layers), _ptr(caches), _ptr(q_begin), _ptr(ctx_len),
-                                     _ptr(path), path.shape[1], _ptr(path_len), _ptr(new_len), _ptr(ws), _bytes(ws),
-                                     _stream(stream)))
+    dev, B, cap = ws.get_device(), d.batch, path.shape[-1]
+    _call_on(dev, stream, (_lib or load()).tb_tree_accept, ctypes.byref(d), n_layers,
+             _at("caches", caches, torch.int64, (2 * n_layers,), dev), _at("q_begin", q_begin, _I32, (B + 1,), dev),
+             _at("ctx_len", ctx_len, _I32, (B,), dev), _at("path", path, _I32, (B, cap), dev), cap,
+             _at("path_len", path_len, _I32, (B,), dev), _at("new_len", new_len, _I32, (B,), dev), ws.data_ptr(),
+             ws.nbytes)
 
 
 def selftest_bounded_wait(ws, budget_cycles: int, stream=None):
