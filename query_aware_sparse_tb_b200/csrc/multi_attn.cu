@@ -66,11 +66,16 @@ template <int D>
 struct Lay {
     static constexpr int kAtoms = D / 64;
     static constexpr int kOperand = 128 * D * 2;  // bytes of a 128-row operand (Q slot, K or V tile)
+    // Tensor memory columns of slot s: S at 128 s.  At 64 head dims the sums
+    // leave room for P beside S, so the next S can be worked out while the
+    // softmax of the current one runs; at 128 P overwrites its S.
+    static constexpr bool kSepP = D == 64;
+    static constexpr uint32_t kO = 256, kOStep = D, kP = kSepP ? 384 : 0, kPStep = kSepP ? 64 : 128;
     // K and V tiles share one ring: 160 KB in flight covers the latency of HBM
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kOperand;
     static constexpr int kBar = kRing + kStages * kOperand;
-    static constexpr int kNumBars = 2 * kStages + 21;
+    static constexpr int kNumBars = 2 * kStages + 23;
     static constexpr int kMisc = kBar + kNumBars * 8;       // TMEM base, abort flag
     static constexpr int kSeg = (kMisc + 8 + 15) / 16 * 16; // two segment descriptions
     static constexpr int kState = kSeg + 2 * 64;            // the slots' m and l [2 slots][2][128]
@@ -256,7 +261,7 @@ struct Params {
     const uint32_t *mask;   // nullptr: causal
     uint16_t *out;
     float *part;            // shares: two states per CTA; nullptr: the counter deals whole items out
-    int32_t *joins;         // shares: one entry per CTA (the item that ends in its first segment)
+    int32_t *joins;         // shares: one entry per CTA (the item begun earlier that ends in it)
     uint32_t *flags, *counter;  // counter[0]: next item, counter[1]: CTAs done
     int batch, Hq, Hkv, cap, n_tokens, max_new, mask_words;
     int g_shift;            // G = 1 << g_shift heads per group
@@ -291,14 +296,20 @@ struct Seq {
     int b, begin, n, kept, T;
 };
 __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
-    Seq q;
-    q.b = b;
-    const SeqSpan sp = seq_span(p.q_begin, b, p.n_tokens);
-    q.begin = sp.begin;
-    q.n = sp.n;
-    q.kept = min(sp.n, p.max_new);
-    q.T = sp.n > 0 ? clamp_ctx(p.ctx_len[b], p.cap, nullptr, false) : 0;
+    Seq q{b, 0, 0, 0, 1};
+    if (b < p.batch) {
+        const SeqSpan sp = seq_span(p.q_begin, b, p.n_tokens);
+        q.begin = sp.begin;
+        q.n = sp.n;
+        q.kept = min(sp.n, p.max_new);
+        q.T = clamp_ctx(p.ctx_len[b], p.cap, nullptr, false);
+    }
     return q;
+}
+__device__ __forceinline__ Seq shfl_seq(const Seq &q, int lane) {
+    return {__shfl_sync(kFullMask, q.b, lane), __shfl_sync(kFullMask, q.begin, lane),
+            __shfl_sync(kFullMask, q.n, lane), __shfl_sync(kFullMask, q.kept, lane),
+            __shfl_sync(kFullMask, q.T, lane)};
 }
 __device__ __forceinline__ int items_of(const Params &p, int kept) {
     const int tpi = kItemRows >> p.g_shift;
@@ -313,25 +324,27 @@ __device__ __forceinline__ int item_tiles(const Params &p, const Seq &q, int ite
     const int tpi = kItemRows >> p.g_shift;
     return tiles_upto(p, q, min((item + 1) * tpi, q.kept) - 1);
 }
+template <typename T>
+__device__ __forceinline__ T warp_prefix(T v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(kFullMask, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
 
 // All lanes of a warp: sequence and number within it of item `tau`, counted
 // over the sequences in packing order.
-__device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, int &b, int &item) {
+__device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, Seq &q, int &item) {
     int before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        int n = 0;
-        if (b0 + lane < p.batch) n = min(seq_span(p.q_begin, b0 + lane, p.n_tokens).n, p.max_new);
-        const int items = items_of(p, n);
-        int incl = items;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFullMask, incl, o);
-            if (lane >= o) incl += v;
-        }
+        const Seq mine = load_seq(p, b0 + lane);
+        const int items = items_of(p, mine.kept), incl = warp_prefix(items, lane);
         const uint32_t hit = __ballot_sync(kFullMask, tau < before + incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            b = b0 + l;
+            q = shfl_seq(mine, l);
             item = tau - before - __shfl_sync(kFullMask, incl - items, l);
             return true;
         }
@@ -341,25 +354,39 @@ __device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, in
 }
 
 // Shares: the tiles of all items in one line (sequences in packing order, its
-// items in order, KV heads inside an item).  All lanes of a warp.  Tiles of
-// one sequence over all its items and KV heads:
-__device__ __forceinline__ long long seq_tiles(const Params &p, int b) {
-    const Seq q = load_seq(p, b);
+// items in order, KV heads inside an item), a tile as long as it takes: about
+// 8 units for 256 rows, 5 for 128 (3,100 cycles against 1,900 with the loads).
+__device__ __forceinline__ int tile_units(const Params &p, const Seq &q, int item) {
+    return min(kItemRows >> p.g_shift, q.kept - item * (kItemRows >> p.g_shift)) > (kSlotRows >> p.g_shift) ? 8 : 5;
+}
+// One sequence's part of the line.
+__device__ __forceinline__ long long seq_units(const Params &p, const Seq &q) {
     const int items = items_of(p, q.kept);
+    if (items == 0) return 0;
     long long t = 0;
-    if (p.mask) {
-        t = (long long)items * tiles_upto(p, q, 0);
+    if (p.mask) {  // all items see all tiles, and all but the last are full
+        t = (long long)tiles_upto(p, q, 0) * (8 * (items - 1) + tile_units(p, q, items - 1));
     } else {
-        for (int i = 0; i < items; ++i) t += item_tiles(p, q, i);
+        for (int i = 0; i < items; ++i) t += item_tiles(p, q, i) * tile_units(p, q, i);
     }
     return t * p.Hkv;
 }
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
-    return v;
-}
-__device__ __forceinline__ long long share_begin(long long total, int c, int ctas) { return total * c / ctas; }
+// The line in `ctas` shares that differ by one unit at most.
+struct Shares {
+    long long total, each;
+    int rest, ctas;
+    __device__ __forceinline__ Shares(long long units, int grid) : total(units) {
+        // no share is below 4 tiles: short contexts keep to fewer CTAs
+        ctas = (int)min((long long)grid, max(1LL, units >> 5));
+        each = units / ctas;
+        rest = (int)(units - each * ctas);
+    }
+    __device__ __forceinline__ long long begin(int c) const { return c >= ctas ? total : each * c + min(c, rest); }
+    __device__ __forceinline__ int holding(long long u) const {  // the share with unit u
+        const long long big = (each + 1) * rest;
+        return (int)(u < big ? u / (each + 1) : rest + (u - big) / each);
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -387,6 +414,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     auto p_full = [&](int s, int half) { return bar(kB + 13 + 2 * s + half); };  // keys 0..63, 64..127
     auto o_done = [&](int s) { return bar(kB + 17 + s); };
     const uint32_t loaded = bar(kB + 20);
+    auto s_read = [&](int s) { return bar(kB + 21 + s); };
     auto tail_done = [&](int i) { return bar(i ? kB + 19 : kB + 2); };
     auto seg = [&](int i) { return reinterpret_cast<volatile int *>(sm + L::kSeg + i * 64); };
 
@@ -408,6 +436,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             mbar_init(seg_empty(s), 10);
             mbar_init(tail_done(s), 1);
             mbar_init(s_full(s), 1);
+            mbar_init(s_read(s), 4);
             mbar_init(p_full(s, 0), 4);
             mbar_init(p_full(s, 1), 4);
             mbar_init(o_done(s), 1);
@@ -420,8 +449,6 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    griddep_wait();
-    griddep_launch_dependents();
     if (warp == 8) {
         tmem_alloc(sb + L::kMisc, kTmemCols);
         tmem_relinquish();
@@ -429,6 +456,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (up to here nothing in global memory was touched)
+    griddep_wait();
+    griddep_launch_dependents();
     const uint32_t tmem = (uint32_t)misc[0];
     const int tps = kSlotRows >> p.g_shift;  // tokens per slot
 
@@ -482,19 +512,23 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             };
             if (p.part == nullptr) {
                 // from the last item to the first: a sequence's last tokens have the most tiles
+                bool first_item = true;
                 while (ok) {
                     // the next item is taken when the current one's last tiles
                     // are on their way: early enough to overlap, and no CTA
                     // holds a second long item while others run dry
                     if (k > 0) ok = wait_warp(loaded, (k - 1) & 1, abort_flag, p.flags);
                     if (!ok) break;
-                    int next = 0;
-                    if (lane == 0) next = (int)atomicAdd(p.counter, 1u);
-                    next = __shfl_sync(kFullMask, next, 0);
+                    int next = blockIdx.x;  // the first item needs no counter
+                    if (!first_item) {
+                        if (lane == 0) next = (int)(gridDim.x + atomicAdd(p.counter, 1u));
+                        next = __shfl_sync(kFullMask, next, 0);
+                    }
+                    first_item = false;
                     if (next >= p.item_bound * p.Hkv) break;
-                    int b, item;
-                    if (!find_item(p, p.item_bound - 1 - next / p.Hkv, lane, b, item)) continue;
-                    const Seq q = load_seq(p, b);
+                    Seq q;
+                    int item;
+                    if (!find_item(p, p.item_bound - 1 - next / p.Hkv, lane, q, item)) continue;
                     const int g = next % p.Hkv, tiles = item_tiles(p, q, item);
                     if (item == 0 && g == 0) report(q);
                     if (tiles > 0)
@@ -504,72 +538,63 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
             } else {
                 const int cta = blockIdx.x;
-                long long total = 0;
-                for (int b0 = 0; b0 < p.batch; b0 += 32)
-                    total += warp_sum(b0 + lane < p.batch ? seq_tiles(p, b0 + lane) : 0);
-                // no share is below 4 tiles: short contexts keep to fewer CTAs
-                const int ctas = (int)min((long long)gridDim.x, max(1LL, total / 4));
-                long long w = cta < ctas ? share_begin(total, cta, ctas) : total;
-                const long long w1 = cta < ctas ? share_begin(total, cta + 1, ctas) : total;
+                const Seq seq0 = load_seq(p, lane);  // of the first 32 sequences
+                const long long units0 = warp_prefix(seq_units(p, seq0), lane);
+                long long total = __shfl_sync(kFullMask, units0, 31);
+                for (int b0 = 32; b0 < p.batch; b0 += 32)
+                    total += __shfl_sync(kFullMask, warp_prefix(seq_units(p, load_seq(p, b0 + lane)), lane), 31);
+                const Shares sh(total, gridDim.x);
+                long long w = sh.begin(cta);
+                const long long w1 = sh.begin(cta + 1);
                 int join_from = -1, join_tok = 0, join_head = 0, join_rows = 0;
-                // the sequence that holds w: `at` is where its line begins
+                // the sequence that holds unit w: `at` is where its part of the line begins
                 long long at = 0;
-                int b = 0;
-                for (int b0 = 0; b0 < p.batch; b0 += 32) {
-                    const long long mine = b0 + lane < p.batch ? seq_tiles(p, b0 + lane) : 0;
-                    long long incl = mine;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const long long v = __shfl_up_sync(kFullMask, incl, o);
-                        if (lane >= o) incl += v;
-                    }
+                int b = p.batch;
+                Seq q;
+                for (int b0 = 0; w < w1 && b0 < p.batch; b0 += 32) {
+                    const Seq mine = b0 == 0 ? seq0 : load_seq(p, b0 + lane);
+                    const long long incl = b0 == 0 ? units0 : warp_prefix(seq_units(p, mine), lane);
                     const uint32_t hit = __ballot_sync(kFullMask, w < at + incl);
                     if (hit) {
                         const int l = __ffs(hit) - 1;
                         b = b0 + l;
-                        at += __shfl_sync(kFullMask, incl - mine, l);
+                        q = shfl_seq(mine, l);
+                        if (l > 0) at += __shfl_sync(kFullMask, incl, l - 1);
                         break;
                     }
                     at += __shfl_sync(kFullMask, incl, 31);
-                    b = min(b0 + 32, p.batch);
                 }
-                for (bool head = true; ok && w < w1 && b < p.batch; ++b) {
-                    const Seq q = load_seq(p, b);
+                while (ok && w < w1 && b < p.batch) {
                     const int items = items_of(p, q.kept);
                     for (int i = 0; i < items && ok && w < w1; ++i) {
-                        const int tiles = item_tiles(p, q, i);
-                        if (w >= at + (long long)tiles * p.Hkv) {
-                            at += (long long)tiles * p.Hkv;
-                            continue;
-                        }
-                        for (int g = (int)((w - at) / max(tiles, 1)); g < p.Hkv && ok && w < w1; ++g) {
-                            const long long a = at + (long long)g * tiles;
-                            const int first = (int)(w - a), last = (int)min((long long)tiles, w1 - a);
-                            const bool whole = first == 0 && last == tiles;
-                            emit(q, i, g, first, last, whole ? -1 : 2 * cta + (head ? 0 : 1));
-                            if (head && first > 0 && last == tiles) {
-                                // this item began in an earlier CTA and ends here
-                                int c0 = (int)(a * ctas / total);
-                                while (share_begin(total, c0 + 1, ctas) <= a) ++c0;
-                                while (share_begin(total, c0, ctas) > a) --c0;
-                                join_from = 2 * c0 + (share_begin(total, c0, ctas) == a ? 0 : 1);
+                        const int tiles = item_tiles(p, q, i), unit = tile_units(p, q, i);
+                        const long long len = (long long)tiles * unit;
+                        for (int g = 0; g < p.Hkv && ok && w < w1; ++g, at += len) {
+                            if (w >= at + len) continue;
+                            // the tiles that begin in this share
+                            const int first = (int)((w - at + unit - 1) / unit);
+                            const int last = (int)min((long long)tiles, (w1 - at + unit - 1) / unit);
+                            w = min(at + len, w1);
+                            if (first >= last) continue;
+                            // states: 2 c for an item begun in an earlier share, 2 c + 1 for one that goes on in the next
+                            emit(q, i, g, first, last, first == 0 && last == tiles ? -1 : 2 * cta + (first == 0));
+                            if (first > 0 && last == tiles) {  // begun earlier, ends here
                                 const int tok0 = i * 2 * tps;
+                                join_from = sh.holding(at);
                                 join_tok = q.begin + tok0;
                                 join_head = g << p.g_shift;
                                 join_rows = min(2 * tps, q.kept - tok0) << p.g_shift;
                             }
-                            head = false;
-                            w = a + last;
                         }
-                        at += (long long)tiles * p.Hkv;
                     }
+                    if (++b < p.batch) q = load_seq(p, b);
                 }
                 if (cta == 0) {  // the lengths' report, and items without a tile, which are in nobody's share
                     for (int b0 = 0; b0 < p.batch; b0 += 32) {
                         bool odd = false;
                         if (b0 + lane < p.batch) {
                             const Seq q = load_seq(p, b0 + lane);
-                            const int t = q.n > 0 ? p.ctx_len[q.b] : 1;
+                            const int t = q.n > 0 ? p.ctx_len[q.b] : 1;  // (an idle sequence's length is not looked at)
                             odd = t < 1 || t > p.cap || (q.n > 0 && q.n > q.T) || q.n > p.max_new;
                         }
                         for (uint32_t hits = __ballot_sync(kFullMask, odd); hits; hits &= hits - 1) {
@@ -596,8 +621,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             __syncwarp();
         } else if (warp == 9) {
             // ======================================================== loads
-            // Ring order = the order in which the products use the tiles: in
-            // pairs K0 V0 K1 V1 ..; else K0 K1 V0 K2 V1 .. V(n-2) V(n-1).
+            // Ring order = the order in which the products use the tiles: K0
+            // V0 K1 V1 .. in pairs, K0 K1 V0 K2 V1 .. for every other tile, and
+            // one more K ahead where the next S does not wait for P.
             int stage = 0, issued = 0, tails = 0, queries = 0, k = 0;
             uint32_t parity = 1;  // of a stage's previous release (passes at once in the first round)
             bool ok = true;
@@ -636,18 +662,12 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         parity ^= 1u;
                     }
                 };
-                if (pair) {
-                    for (int t = 0; t < nt && ok; ++t) {
-                        load(true, t);
-                        load(false, t);
-                    }
-                } else {
-                    if (nt > 0) load(true, 0);
-                    if (nt > 1) load(true, 1);
-                    for (int t = 0; t < nt && ok; ++t) {
-                        load(false, t);
-                        if (t + 2 < nt) load(true, t + 2);
-                    }
+                // K tiles run `ahead` tiles before V
+                const int ahead = (pair ? 0 : 1) + (L::kSepP ? 1 : 0);
+                for (int t = 0; t <= ahead && t < nt; ++t) load(true, t);
+                for (int t = 0; t < nt && ok; ++t) {
+                    load(false, t);
+                    if (t + ahead + 1 < nt) load(true, t + ahead + 1);
                 }
                 if (!ok) break;
                 if (tail > 0) {
@@ -693,7 +713,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const uint32_t q_lo = (uint32_t)kd, hi = (uint32_t)(kd >> 32);
                 const uint32_t k_lo = q_lo + (L::kRing >> 4), v_lo = (uint32_t)vd;
                 int k_stage = 0, v_stage = 0, next = 0;
-                uint32_t next_parity = 0, tails = 0, done = 0;  // done: bit s = parity of slot s's tiles so far
+                uint32_t next_parity = 0, tails = 0;
+                uint32_t done = 0, read = 0;  // bit s = parity of slot s's tiles so far (P used, S read)
                 bool ok = true;
                 auto acquire = [&](int &st) {
                     st = next;
@@ -713,57 +734,74 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     ok = wait_role(q_full, k & 1, abort_flag, p.flags);
                     // step i belongs to slot i & 1; in pairs steps 2t and 2t+1
                     // use tile t, else step i uses tile i.  Each round: the
-                    // step's PV, then the same slot's next S.
+                    // step's PV, then the same slot's next S, which overwrites
+                    // the columns of P (PV has read them by then: the products
+                    // of one thread run in order); where P has columns of its
+                    // own, the next S first, once the softmax has read the last.
                     const int steps = pair ? 2 * nt : nt;
+                    auto next_s = [&](int i) {
+                        const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
+                        const bool first = !pair || slot == 0, last = !pair || slot == 1;
+                        if (i + 2 >= steps) return;
+                        if (first) acquire(k_stage);
+                        if (ok && j + 1 < n_slot) {
+                            if (L::kSepP && i >= 0) {
+                                ok = wait_role(s_read(slot), (read >> slot) & 1u, abort_flag, p.flags);
+                                read ^= 1u << slot;
+                            }
+                            if (!ok) return;
+                            tc_fence_after();
+                            const uint32_t q = q_lo + (pair ? slot : 0) * kStep, kl = k_lo + k_stage * kStep;
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t o = (uint32_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+                                umma_ss(tmem + slot * 128, q + o, kl + o, hi, id_s, kk > 0);
+                            }
+                            umma_commit(s_full(slot));
+                        }
+                        if (!ok) return;
+                        if (last) umma_commit(empty(k_stage));
+                        if (i + 3 == steps) umma_commit(q_empty);  // the segment's last S
+                    };
 #pragma unroll 1
                     for (int i = -2; i < steps && ok; ++i) {
                         const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
                         const bool first = !pair || slot == 0, last = !pair || slot == 1;
-                        if (i >= 0) {
-                            if (first) {
-                                acquire(v_stage);
-                                if (tail > 0 && (pair ? j : i) + 1 == nt && ok) {
-                                    ok = wait_role(tail_done(tails & 1), (tails >> 1) & 1u, abort_flag, p.flags);
-                                    ++tails;
-                                }
-                                // the previous segment's sums have been read
-                                if (i == 0 && k > 0 && ok) ok = wait_role(o_free, (k - 1) & 1, abort_flag, p.flags);
+                        if (L::kSepP || i < 0) next_s(i);
+                        if (i < 0 || !ok) continue;
+                        if (first) {
+                            acquire(v_stage);
+                            if (tail > 0 && (pair ? j : i) + 1 == nt && ok) {
+                                ok = wait_role(tail_done(tails & 1), (tails >> 1) & 1u, abort_flag, p.flags);
+                                ++tails;
                             }
-                            if (j < n_slot) {
-                                const uint32_t v = v_lo + v_stage * kStep;
+                            // the previous segment's sums have been read
+                            if (i == 0 && k > 0 && ok) ok = wait_role(o_free, (k - 1) & 1, abort_flag, p.flags);
+                        }
+                        if (j < n_slot) {
+                            const uint32_t v = v_lo + v_stage * kStep;
 #pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    if (ok) ok = wait_role(p_full(slot, half), (done >> slot) & 1u, abort_flag, p.flags);
-                                    if (!ok) break;
-                                    tc_fence_after();
-#pragma unroll
-                                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                                        umma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, v + kk * 128, hi,
-                                                id_o, (j | kk) ? 1u : 0u);
-                                }
+                            for (int half = 0; half < 2; ++half) {
+                                if (ok) ok = wait_role(p_full(slot, half), (done >> slot) & 1u, abort_flag, p.flags);
                                 if (!ok) break;
-                                umma_commit(o_done(slot));
-                                done ^= 1u << slot;
-                            }
-                            if (!ok) break;
-                            if (last) umma_commit(empty(v_stage));
-                        }
-                        if (i + 2 < steps) {
-                            if (first) acquire(k_stage);
-                            if (!ok) break;
-                            if (j + 1 < n_slot) {
                                 tc_fence_after();
-                                const uint32_t q = q_lo + (pair ? slot : 0) * kStep, kl = k_lo + k_stage * kStep;
 #pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk) {
-                                    const uint32_t o = (uint32_t)((kk >> 2) * 1024 + (kk & 3) * 2);
-                                    umma_ss(tmem + slot * 128, q + o, kl + o, hi, id_s, kk > 0);
-                                }
-                                umma_commit(s_full(slot));
+                                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                                    umma_ts(tmem + L::kO + slot * L::kOStep, tmem + L::kP + slot * L::kPStep + kk * 8,
+                                            v + kk * 128, hi, id_o, (j | kk) ? 1u : 0u);
                             }
-                            if (last) umma_commit(empty(k_stage));
-                            if (i + 3 == steps) umma_commit(q_empty);  // the segment's last S
+                            if (!ok) break;
+                            umma_commit(o_done(slot));
+                            done ^= 1u << slot;
                         }
+                        if (!ok) break;
+                        if (last) umma_commit(empty(v_stage));
+                        if (!L::kSepP) next_s(i);
+                    }
+                    if (L::kSepP && ok) {
+                        // each slot's last S was read too: keep the barriers' phases in step
+                        for (int slot = 0; slot < 2; ++slot)
+                            if ((slot ? nt1 : nt0) > 0) read ^= 1u << slot;
                     }
                     if (!ok) break;
                     mbar_arrive(seg_empty(k & 1));
@@ -779,7 +817,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int slot = warp >> 2;
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_base + slot * 128, to = tmem + lane_base + 256;
+        const uint32_t ts = tmem + lane_base + slot * 128, to = tmem + lane_base + L::kO;
+        const uint32_t tp = tmem + lane_base + L::kP + slot * L::kPStep;
         uint32_t count = 0, merges = 0;  // tiles of this slot so far; merged segments so far
         uint32_t other_count = 0;        // tiles of the other slot so far
         bool ok = true;
@@ -842,6 +881,11 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait32(s[q]);
+                if (L::kSepP) {  // the next S may overwrite this one
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_read(slot));
+                }
                 if (masked) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -864,21 +908,26 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 // a NaN or +inf logit makes the row's softmax NaN: so becomes m, and l with it
                 if (!(top < INFINITY)) top = NAN;
                 const bool raise = !(top <= m + kLazy);  // also the first logit of a row (m = -inf)
+                if (L::kSepP && j > 0) {  // the previous P has been read
+                    ok = wait_warp(o_done(slot), (count - 1) & 1, abort_flag, p.flags);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 if (__any_sync(kFullMask, raise)) {
                     const float m_new = raise ? top : m;
                     const float fac = m_new == m ? 1.f : ex2(m - m_new);  // (-inf stays -inf while nothing is seen)
                     if (j > 0) {
-                        ok = wait_warp(o_done(slot), (count - 1) & 1, abort_flag, p.flags);
+                        if (!L::kSepP) ok = wait_warp(o_done(slot), (count - 1) & 1, abort_flag, p.flags);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < D / 16; ++q) {  // rare: kept small, the logits fill the registers
                             float o[16];
                             uint32_t w[16];
-                            tmem_ld16(to + slot * 128 + q * 16, o);
+                            tmem_ld16(to + slot * L::kOStep + q * 16, o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * fac);
-                            tmem_st16(to + slot * 128 + q * 16, w);
+                            tmem_st16(to + slot * L::kOStep + q * 16, w);
                         }
                     }
                     l *= fac;
@@ -907,7 +956,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         // per weight, below the rounding of the bf16 result
                         w[i] = pack_bf16(e0, e1);
                     }
-                    tmem_st16(ts + q * 16, w);
+                    tmem_st16(tp + q * 16, w);
                     if (q & 1) {  // half of the weights are in place
                         tmem_wait_st();
                         tc_fence_before();
@@ -970,12 +1019,12 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 float o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                if (n_mine > 0) tmem_ld16(to + slot * 128 + q * 16, o);
+                if (n_mine > 0) tmem_ld16(to + slot * L::kOStep + q * 16, o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] *= f0;
                 if (!pair && n_other > 0) {
                     float o1[16];
-                    tmem_ld16(to + (slot ^ 1) * 128 + q * 16, o1);
+                    tmem_ld16(to + (slot ^ 1) * L::kOStep + q * 16, o1);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = fmaf(o1[i], f1, o[i]);
                 }
@@ -1044,7 +1093,7 @@ multi_join_kernel(const Params p) {
     const int32_t *e = p.joins + 4 * blockIdx.x;
     const int from = e[0], tok = e[1], head = e[2], rows = e[3];
     if (from < 0 || (int)blockIdx.y * 32 >= rows) return;
-    const int n = (int)blockIdx.x - (from >> 1) + 1;  // CTAs from >> 1 .. blockIdx.x, the first one's state `from`
+    const int n = (int)blockIdx.x - from + 1;  // CTAs from .. blockIdx.x: state 2 c + 1 of the first, 2 c of the others
     constexpr size_t kRec = (size_t)(D + 2) * kItemRows;
     const int d0 = blockIdx.z * 32 + warp * 8;
     const float *base = p.part + blockIdx.y * 32 + lane;
@@ -1059,7 +1108,7 @@ multi_join_kernel(const Params p) {
             ms[u] = -INFINITY;
             ls[u] = 0.f;
             if (s0 + u < n) {
-                const float *r = base + (size_t)(s0 + u ? 2 * ((from >> 1) + s0 + u) : from) * kRec;
+                const float *r = base + (size_t)(2 * (from + s0 + u) + (s0 + u == 0)) * kRec;
                 ms[u] = r[(size_t)D * kItemRows];
                 ls[u] = r[(size_t)(D + 1) * kItemRows];
 #pragma unroll
