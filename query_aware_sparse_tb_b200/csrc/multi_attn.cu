@@ -59,7 +59,7 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;               // log2 units
-constexpr int kPolyOf8 = 3;                 // of 8 pairs of weights, those worked out on the FMA pipe
+constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 template <int D>
@@ -261,7 +261,7 @@ struct Params {
     const uint32_t *mask;   // nullptr: causal
     uint16_t *out;
     float *part;            // shares: two states per CTA; nullptr: the counter deals whole items out
-    int32_t *joins;         // shares: one entry per CTA (the item begun earlier that ends in it)
+    int32_t *joins;         // shares: what to join, 8 words an entry (first CTA or -1, CTAs, token, head, rows)
     uint32_t *flags, *counter;  // counter[0]: next item, counter[1]: CTAs done
     int batch, Hq, Hkv, cap, n_tokens, max_new, mask_words;
     int g_shift;            // G = 1 << g_shift heads per group
@@ -270,6 +270,10 @@ struct Params {
 };
 
 // A segment as warp 10 describes it to the others.
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
 enum SegField {
     kEnd,        // 1: no further segment
     kPair,       // slots: 1 = two row blocks over the same tiles, 0 = one row block, every other tile
@@ -354,20 +358,43 @@ __device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, Se
 }
 
 // Shares: the tiles of all items in one line (sequences in packing order, its
-// items in order, KV heads inside an item), a tile as long as it takes: about
-// 8 units for 256 rows, 5 for 128 (3,100 cycles against 1,900 with the loads).
+// items in order, KV heads inside an item), each as long as it takes.  A tile
+// of 256 rows takes 3,100 cycles; one of 128 rows takes 1,900, or what its
+// bytes take from HBM (2,600) where no other item reads them: 7 to 5.
+// An item's first tile counts one more, for its start and its epilogue.
 __device__ __forceinline__ int tile_units(const Params &p, const Seq &q, int item) {
-    return min(kItemRows >> p.g_shift, q.kept - item * (kItemRows >> p.g_shift)) > (kSlotRows >> p.g_shift) ? 8 : 5;
+    const bool pair = min(kItemRows >> p.g_shift, q.kept - item * (kItemRows >> p.g_shift)) > (kSlotRows >> p.g_shift);
+    return pair ? 7 : 5;
+}
+__device__ __forceinline__ long long item_units(int tiles, int unit) { return tiles > 0 ? (long long)(tiles + 1) * unit : 0; }
+// The first tile that begins at or behind unit x of an item.
+__device__ __forceinline__ int tile_behind(long long x, int unit) {
+    return x <= 0 ? 0 : (int)max(1LL, (x + unit - 1) / unit - 1);
 }
 // One sequence's part of the line.
 __device__ __forceinline__ long long seq_units(const Params &p, const Seq &q) {
     const int items = items_of(p, q.kept);
     if (items == 0) return 0;
-    long long t = 0;
-    if (p.mask) {  // all items see all tiles, and all but the last are full
-        t = (long long)tiles_upto(p, q, 0) * (8 * (items - 1) + tile_units(p, q, items - 1));
-    } else {
-        for (int i = 0; i < items; ++i) t += item_tiles(p, q, i) * tile_units(p, q, i);
+    const int base = q.T - q.n, last = items - 1;
+    long long t = item_units(item_tiles(p, q, last), tile_units(p, q, last));
+    if (last > 0) {  // the full items
+        const int unit = tile_units(p, q, 0);
+        if (p.mask) {
+            t += last * item_units(tiles_upto(p, q, 0), unit);
+        } else if (base < 0) {
+            for (int i = 0; i < last; ++i) t += item_units(item_tiles(p, q, i), unit);
+        } else {
+            // sum of ceil((base + i tpi) / 128) over i = 1 .. last: every `k`
+            // items (k = 128 / tpi) the tiles grow by `d`
+            const int tpi = kItemRows >> p.g_shift, k = max(1, kTile / tpi), d = max(1, tpi / kTile);
+            const long long blocks = last / k;
+            long long tiles = 0;
+            for (int r = 1; r <= k; ++r) {  // i = r, r + k, ..: `count` of them
+                const long long count = blocks + (r <= last % k);
+                tiles += count * ((base + r * tpi + kTile - 1) / kTile) + d * (count * (count - 1) / 2);
+            }
+            t += (tiles + last) * unit;
+        }
     }
     return t * p.Hkv;
 }
@@ -540,78 +567,102 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const int cta = blockIdx.x;
                 const Seq seq0 = load_seq(p, lane);  // of the first 32 sequences
                 const long long units0 = warp_prefix(seq_units(p, seq0), lane);
+                const int items0 = warp_prefix(items_of(p, seq0.kept), lane);
                 long long total = __shfl_sync(kFullMask, units0, 31);
-                for (int b0 = 32; b0 < p.batch; b0 += 32)
-                    total += __shfl_sync(kFullMask, warp_prefix(seq_units(p, load_seq(p, b0 + lane)), lane), 31);
+                int total_items = __shfl_sync(kFullMask, items0, 31);
+                for (int b0 = 32; b0 < p.batch; b0 += 32) {
+                    const Seq mine = load_seq(p, b0 + lane);
+                    total += __shfl_sync(kFullMask, warp_prefix(seq_units(p, mine), lane), 31);
+                    total_items += __shfl_sync(kFullMask, warp_prefix(items_of(p, mine.kept), lane), 31);
+                }
+                total_items *= p.Hkv;
                 const Shares sh(total, gridDim.x);
                 long long w = sh.begin(cta);
                 const long long w1 = sh.begin(cta + 1);
-                int join_from = -1, join_tok = 0, join_head = 0, join_rows = 0;
+                // an entry for every item, or where there are more items than
+                // CTAs, for every CTA (one item at most ends in it that began earlier)
+                const bool by_item = p.item_bound * p.Hkv <= (int)gridDim.x;
+                auto join = [&](int entry, int from, int tok, int head, int rows) {
+                    if (lane == 0) *reinterpret_cast<int4 *>(p.joins + 8 * entry) = make_int4(from, cta - from + 1, tok, head);
+                    if (lane == 0) p.joins[8 * entry + 4] = rows;
+                };
+                bool joined = false;
                 // the sequence that holds unit w: `at` is where its part of the line begins
                 long long at = 0;
-                int b = p.batch;
+                int b = p.batch, items_before = 0;
                 Seq q;
                 for (int b0 = 0; w < w1 && b0 < p.batch; b0 += 32) {
                     const Seq mine = b0 == 0 ? seq0 : load_seq(p, b0 + lane);
                     const long long incl = b0 == 0 ? units0 : warp_prefix(seq_units(p, mine), lane);
+                    const int before = b0 == 0 ? items0 : warp_prefix(items_of(p, mine.kept), lane);
                     const uint32_t hit = __ballot_sync(kFullMask, w < at + incl);
                     if (hit) {
                         const int l = __ffs(hit) - 1;
                         b = b0 + l;
                         q = shfl_seq(mine, l);
                         if (l > 0) at += __shfl_sync(kFullMask, incl, l - 1);
+                        if (l > 0) items_before += __shfl_sync(kFullMask, before, l - 1);
                         break;
                     }
                     at += __shfl_sync(kFullMask, incl, 31);
+                    items_before += __shfl_sync(kFullMask, before, 31);
                 }
                 while (ok && w < w1 && b < p.batch) {
                     const int items = items_of(p, q.kept);
                     for (int i = 0; i < items && ok && w < w1; ++i) {
                         const int tiles = item_tiles(p, q, i), unit = tile_units(p, q, i);
-                        const long long len = (long long)tiles * unit;
+                        const long long len = item_units(tiles, unit);
+                        if (w >= at + len * p.Hkv) {
+                            at += len * p.Hkv;
+                            continue;
+                        }
                         for (int g = 0; g < p.Hkv && ok && w < w1; ++g, at += len) {
                             if (w >= at + len) continue;
                             // the tiles that begin in this share
-                            const int first = (int)((w - at + unit - 1) / unit);
-                            const int last = (int)min((long long)tiles, (w1 - at + unit - 1) / unit);
+                            const int first = tile_behind(w - at, unit);
+                            const int last = min(tiles, tile_behind(w1 - at, unit));
                             w = min(at + len, w1);
                             if (first >= last) continue;
                             // states: 2 c for an item begun in an earlier share, 2 c + 1 for one that goes on in the next
                             emit(q, i, g, first, last, first == 0 && last == tiles ? -1 : 2 * cta + (first == 0));
-                            if (first > 0 && last == tiles) {  // begun earlier, ends here
+                            if (last == tiles && (first > 0 || by_item)) {  // ends here
                                 const int tok0 = i * 2 * tps;
-                                join_from = sh.holding(at);
-                                join_tok = q.begin + tok0;
-                                join_head = g << p.g_shift;
-                                join_rows = min(2 * tps, q.kept - tok0) << p.g_shift;
+                                join(by_item ? (items_before + i) * p.Hkv + g : cta, first > 0 ? sh.holding(at) : -1,
+                                     q.begin + tok0, g << p.g_shift, min(2 * tps, q.kept - tok0) << p.g_shift);
+                                joined = true;
                             }
                         }
                     }
+                    items_before += items;
                     if (++b < p.batch) q = load_seq(p, b);
                 }
                 if (cta == 0) {  // the lengths' report, and items without a tile, which are in nobody's share
+                    int before = 0;
                     for (int b0 = 0; b0 < p.batch; b0 += 32) {
                         bool odd = false;
+                        const Seq mine = load_seq(p, b0 + lane);
+                        const int upto = before + warp_prefix(items_of(p, mine.kept), lane);
+                        before = __shfl_sync(kFullMask, upto, 31);
                         if (b0 + lane < p.batch) {
-                            const Seq q = load_seq(p, b0 + lane);
+                            const Seq q = mine;
                             const int t = q.n > 0 ? p.ctx_len[q.b] : 1;  // (an idle sequence's length is not looked at)
                             odd = t < 1 || t > p.cap || (q.n > 0 && q.n > q.T) || q.n > p.max_new;
                         }
                         for (uint32_t hits = __ballot_sync(kFullMask, odd); hits; hits &= hits - 1) {
-                            const Seq q = load_seq(p, b0 + __ffs(hits) - 1);
+                            const int l = __ffs(hits) - 1, items = __shfl_sync(kFullMask, items_of(p, mine.kept), l);
+                            const int at_item = __shfl_sync(kFullMask, upto, l) - items;
+                            const Seq q = shfl_seq(mine, l);
                             report(q);
-                            for (int i = 0; i < items_of(p, q.kept) && item_tiles(p, q, i) == 0; ++i)
-                                for (int g = 0; g < p.Hkv; ++g) zero_item(q, i, g);
+                            for (int i = 0; i < items && item_tiles(p, q, i) == 0; ++i)
+                                for (int g = 0; g < p.Hkv; ++g) {
+                                    zero_item(q, i, g);
+                                    if (by_item) join((at_item + i) * p.Hkv + g, -1, 0, 0, 0);
+                                }
                         }
                     }
                 }
-                if (lane == 0) {
-                    int32_t *e = p.joins + 4 * cta;
-                    e[0] = join_from;
-                    e[1] = join_tok;
-                    e[2] = join_head;
-                    e[3] = join_rows;
-                }
+                // entries nobody else writes: this CTA's, or those behind the last item
+                if (by_item ? cta >= total_items && cta < p.item_bound * p.Hkv : !joined) join(cta, -1, 0, 0, 0);
             }
             if (ok && k >= 2) ok = wait_warp(seg_empty(k & 1), ((k >> 1) + 1) & 1, abort_flag, p.flags);
             if (ok && lane == 0) {
@@ -732,20 +783,21 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     const bool pair = f[kPair];
                     const int nt = f[kTiles], nt0 = f[kTiles0], nt1 = f[kTiles1], tail = f[kTail];
                     ok = wait_role(q_full, k & 1, abort_flag, p.flags);
-                    // step i belongs to slot i & 1; in pairs steps 2t and 2t+1
-                    // use tile t, else step i uses tile i.  Each round: the
-                    // step's PV, then the same slot's next S, which overwrites
+                    // round j: slot 0's and slot 1's step, each the PV of its
+                    // tile j and the S of its tile j + 1.  In pairs both use
+                    // K/V tile j, else tiles 2j and 2j + 1.  The S overwrites
                     // the columns of P (PV has read them by then: the products
                     // of one thread run in order); where P has columns of its
-                    // own, the next S first, once the softmax has read the last.
-                    const int steps = pair ? 2 * nt : nt;
-                    auto next_s = [&](int i) {
-                        const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
-                        const bool first = !pair || slot == 0, last = !pair || slot == 1;
-                        if (i + 2 >= steps) return;
-                        if (first) acquire(k_stage);
-                        if (ok && j + 1 < n_slot) {
-                            if (L::kSepP && i >= 0) {
+                    // own it goes first, once the softmax has read the last.
+                    const int rounds = pair ? nt : (nt + 1) >> 1;
+                    auto next_s = [&](auto slot_c, int j) {
+                        constexpr int slot = decltype(slot_c)::value;
+                        // (in pairs slot 1 has every tile, so it also releases them)
+                        const bool uses = pair ? j + 1 < nt : 2 * (j + 1) + slot < nt;
+                        if (!ok || !uses) return;
+                        if (!pair || slot == 0) acquire(k_stage);
+                        if (j + 1 < (slot ? nt1 : nt0)) {
+                            if (L::kSepP && j >= 0 && ok) {
                                 ok = wait_role(s_read(slot), (read >> slot) & 1u, abort_flag, p.flags);
                                 read ^= 1u << slot;
                             }
@@ -760,44 +812,54 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                             umma_commit(s_full(slot));
                         }
                         if (!ok) return;
-                        if (last) umma_commit(empty(k_stage));
-                        if (i + 3 == steps) umma_commit(q_empty);  // the segment's last S
+                        if (!pair || slot == 1) umma_commit(empty(k_stage));
+                        // the segment's last S: the queries are free
+                        if (pair ? slot == 1 && j + 2 == nt : 2 * (j + 1) + slot + 1 == nt) umma_commit(q_empty);
                     };
-#pragma unroll 1
-                    for (int i = -2; i < steps && ok; ++i) {
-                        const int slot = i & 1, j = i >> 1, n_slot = slot ? nt1 : nt0;
-                        const bool first = !pair || slot == 0, last = !pair || slot == 1;
-                        if (L::kSepP || i < 0) next_s(i);
-                        if (i < 0 || !ok) continue;
-                        if (first) {
+                    auto pv = [&](auto slot_c, int j) {
+                        constexpr int slot = decltype(slot_c)::value;
+                        const int tile = pair ? j : 2 * j + slot;
+                        if (!ok || tile >= nt) return;
+                        if (!pair || slot == 0) {
                             acquire(v_stage);
-                            if (tail > 0 && (pair ? j : i) + 1 == nt && ok) {
+                            if (tail > 0 && tile + 1 == nt && ok) {
                                 ok = wait_role(tail_done(tails & 1), (tails >> 1) & 1u, abort_flag, p.flags);
                                 ++tails;
                             }
                             // the previous segment's sums have been read
-                            if (i == 0 && k > 0 && ok) ok = wait_role(o_free, (k - 1) & 1, abort_flag, p.flags);
+                            if (slot == 0 && j == 0 && k > 0 && ok) ok = wait_role(o_free, (k - 1) & 1, abort_flag, p.flags);
                         }
-                        if (j < n_slot) {
+                        if (j < (slot ? nt1 : nt0)) {
                             const uint32_t v = v_lo + v_stage * kStep;
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 if (ok) ok = wait_role(p_full(slot, half), (done >> slot) & 1u, abort_flag, p.flags);
-                                if (!ok) break;
+                                if (!ok) return;
                                 tc_fence_after();
 #pragma unroll
                                 for (int kk = half * 4; kk < half * 4 + 4; ++kk)
                                     umma_ts(tmem + L::kO + slot * L::kOStep, tmem + L::kP + slot * L::kPStep + kk * 8,
                                             v + kk * 128, hi, id_o, (j | kk) ? 1u : 0u);
                             }
-                            if (!ok) break;
                             umma_commit(o_done(slot));
                             done ^= 1u << slot;
                         }
-                        if (!ok) break;
-                        if (last) umma_commit(empty(v_stage));
-                        if (!L::kSepP) next_s(i);
+                        if (ok && (!pair || slot == 1)) umma_commit(empty(v_stage));
+                    };
+                    using Slot0 = Const<0>;
+                    using Slot1 = Const<1>;
+                    next_s(Slot0{}, -1);
+                    next_s(Slot1{}, -1);
+#pragma unroll 1
+                    for (int j = 0; j < rounds && ok; ++j) {
+                        if (L::kSepP) next_s(Slot0{}, j);
+                        pv(Slot0{}, j);
+                        if (!L::kSepP) next_s(Slot0{}, j);
+                        if (L::kSepP) next_s(Slot1{}, j);
+                        pv(Slot1{}, j);
+                        if (!L::kSepP) next_s(Slot1{}, j);
                     }
+                    if (!ok) break;
                     if (L::kSepP && ok) {
                         // each slot's last S was read too: keep the barriers' phases in step
                         for (int slot = 0; slot < 2; ++slot)
@@ -1079,10 +1141,10 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
 // Joins the states of an item that was shared out:
 //   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-// blockIdx.x is the CTA in whose first segment the item ends (it says so in
-// its entry), y a block of 32 rows (lane = row, so the states are read 128
-// bytes at a time), z a block of 32 head dims, 8 per warp.  The tile is turned
-// in shared memory and stored row by row.
+// blockIdx.x is the entry, y a block of 32 rows (lane = row, so the states are
+// read 128 bytes at a time), z a block of 32 head dims, 8 per warp.  The loads
+// of 8 states are in flight at once: latency is all there is to it.  The tile
+// is turned in shared memory and stored row by row.
 template <int D>
 __global__ void __launch_bounds__(128)
 multi_join_kernel(const Params p) {
@@ -1090,17 +1152,17 @@ multi_join_kernel(const Params p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    const int32_t *e = p.joins + 4 * blockIdx.x;
-    const int from = e[0], tok = e[1], head = e[2], rows = e[3];
+    const int4 e = *reinterpret_cast<const int4 *>(p.joins + 8 * blockIdx.x);
+    const int rows = p.joins[8 * blockIdx.x + 4];
+    const int from = e.x, n = e.y, tok = e.z, head = e.w;  // CTAs from .. from + n - 1: state 2 c + 1 of the first, 2 c of the others
     if (from < 0 || (int)blockIdx.y * 32 >= rows) return;
-    const int n = (int)blockIdx.x - from + 1;  // CTAs from .. blockIdx.x: state 2 c + 1 of the first, 2 c of the others
     constexpr size_t kRec = (size_t)(D + 2) * kItemRows;
     const int d0 = blockIdx.z * 32 + warp * 8;
     const float *base = p.part + blockIdx.y * 32 + lane;
     float M = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     for (int s0 = 0; s0 < n; s0 += kBatch) {
         float ms[kBatch], ls[kBatch], v[kBatch][8];
 #pragma unroll
@@ -1222,7 +1284,8 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
     const unsigned ctas = (unsigned)(p.part || items > sms ? sms : items);
     e = launch_pdl(multi_attn_kernel<D>, dim3(ctas), dim3(kThreads), L::kBytes, st, mQ, mK, mV, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch_pdl(multi_join_kernel<D>, dim3(ctas, kItemRows / 32, D / 32), dim3(128), 0, st, p);
+    return launch_pdl(multi_join_kernel<D>, dim3(items < sms ? (unsigned)items : ctas, kItemRows / 32, D / 32), dim3(128), 0,
+                      st, p);
 }
 
 }  // namespace
@@ -1231,7 +1294,7 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
 size_t multi_attn_ws_bytes(const tb_dims &d, int32_t n_tokens, int32_t max_new, bool tree) {
     if (!use_shares(d, max_new, tree, item_bound(d, n_tokens, max_new))) return kWsHeaderBytes;
     const size_t ctas = (size_t)num_sms();
-    return kWsHeaderBytes + align_up(ctas * 16, 256) + ctas * 2 * (d.head_dim + 2) * kItemRows * sizeof(float);
+    return kWsHeaderBytes + align_up(ctas * 32, 256) + ctas * 2 * (d.head_dim + 2) * kItemRows * sizeof(float);
 }
 
 cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
@@ -1256,7 +1319,7 @@ cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_
     p.item_bound = (int)item_bound(d, n_tokens, max_new);
     if (use_shares(d, max_new, mask != nullptr, p.item_bound)) {
         p.joins = reinterpret_cast<int32_t *>(w + kWsHeaderBytes);
-        p.part = reinterpret_cast<float *>(w + kWsHeaderBytes + align_up((size_t)num_sms() * 16, 256));
+        p.part = reinterpret_cast<float *>(w + kWsHeaderBytes + align_up((size_t)num_sms() * 32, 256));
     }
     p.c = scale * 1.4426950408889634f;
     return d.head_dim == 128 ? launch_d<128>(d, Q, K, V, p, st) : launch_d<64>(d, Q, K, V, p, st);
