@@ -10,8 +10,8 @@
 //
 // over t <= T - n + i (prompt), or t < T - n and the drafted rows whose bit is
 // set (tree).  m is a running reference, not the exact maximum: it is raised
-// only when a logit exceeds it by more than 8 (log2 units), so the accumulator
-// is rescaled rarely; p stays below 2^8 and the sums, held in fp32, are exact
+// only when a logit exceeds it by more than 32 (log2 units), so the accumulator
+// is rescaled rarely; p stays below 2^32 and the sums, held in fp32, are exact
 // up to fp32 rounding either way.
 //
 // Work item: 256 rows of one KV head, a row being (token, head of the group),
@@ -58,7 +58,13 @@ constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazy = 8.0f;               // log2 units
+// How far (log2 units) a logit may exceed the reference m before m is raised.
+// A raise rescales the sums in tensor memory, about 1,000 cycles a tile, and
+// with a few large keys in the context some row of 32 wants one in most of the
+// first tiles.  Weights up to 2^32 lose nothing, bf16 and fp32 having the same
+// exponents; the sums (weights x 2^22 rows x |v|) stay finite to |v| of 2^72.
+// At 8 an 8K prompt with 1% of its keys scaled by 4 took 540 us, at 32 505.
+constexpr float kLazy = 32.0f;
 constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
 constexpr uint32_t kFullMask = 0xffffffffu;
 
@@ -893,6 +899,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const int t_step = pair ? 1 : 2, n_mine = slot ? f[kTiles1] : f[kTiles0];
             const int p_step = t_step * kTile;
             int p0 = (f[kFirst] + (pair ? 0 : slot)) * kTile;  // the tile's first cache row
+            int n_loop = n_mine;
             // the row sees every cache row below all_end, and of the drafted
             // rows from all_end to draft_end those with a bit in mrow
             const uint32_t *mrow = nullptr;
@@ -909,6 +916,24 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 masked_from = p.mask ? base : base + f[kTok0] + (pair ? slot * tps : 0) + 1;
             }
             float m = -INFINITY, l = 0.f;
+            // a warp whose 32 rows all lie behind the item's last token only
+            // keeps the barriers going: its rows' weights and sums are whatever
+            // the columns hold, and nobody reads them
+            if ((pair ? slot * tps : 0) + (((warp & 3) * 32) >> p.g_shift) >= f[kNTok]) {
+                for (int j = 0; j < n_mine; ++j, ++count) {
+                    ok = wait_warp(s_full(slot), count & 1, abort_flag, p.flags);
+                    // (as below: not a tile ahead of the slot's other warps)
+                    if (ok && L::kSepP && j > 0) ok = wait_warp(o_done(slot), (count - 1) & 1, abort_flag, p.flags);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (L::kSepP) mbar_arrive(s_read(slot));
+                        mbar_arrive(p_full(slot, 0));
+                        mbar_arrive(p_full(slot, 1));
+                    }
+                    __syncwarp();
+                }
+                n_loop = 0;
+            }
 
             // which of the 32 cache rows from r on this row attends to
             auto allowed = [&](int r) -> uint32_t {
@@ -928,7 +953,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 return d;
             };
 
-            for (int j = 0; j < n_mine; ++j, p0 += p_step, ++count) {
+            for (int j = 0; j < n_loop; ++j, p0 += p_step, ++count) {
                 const bool masked = p0 + kTile > masked_from;
                 uint32_t see[4];
                 if (masked) {

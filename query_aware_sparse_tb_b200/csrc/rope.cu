@@ -109,22 +109,24 @@ norm_rope_append_kernel(const RopeParams p) {
         ga = l < R ? l : l + R;
         gb = l < R ? l + R : l + LPH;
     }
-    float cs[4], sn[4];
-    if (h0 < p.Hq + p.Hkv && ra) {
+    // cosines and sines of the lane's 4 pairs: the HPI lanes that hold the same
+    // values of different heads work out 4 / HPI of them each and trade
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    if (h0 < p.Hq + p.Hkv && p.rot > 0) {
         const double P = (double)(p.pos ? p.pos[tok] : row);
+        float c[4 / HPI], s[4 / HPI];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int j = p.interleaved ? ga * 2 + k : l * 4 + k;  // (a group that does not turn is not read)
+        for (int i = 0; i < 4 / HPI; ++i) {
+            const int j = 4 * l + i * HPI + lane / LPH;  // the pair's frequency
             double t = 0.0;
             if (j < p.rot / 2) t = P * p.inv_freq[j] * 0.31830988618379067154;  // half turns
             t -= 2.0 * rint(0.5 * t);
-            sincospif((float)t, &sn[k], &cs[k]);
+            sincospif((float)t, &s[i], &c[i]);
         }
-    } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            cs[k] = 1.f;
-            sn[k] = 0.f;
+            cs[k] = __shfl_sync(kFullMask, c[k / HPI], l + LPH * (k % HPI));
+            sn[k] = __shfl_sync(kFullMask, s[k / HPI], l + LPH * (k % HPI));
         }
     }
 
