@@ -23,9 +23,9 @@
 // at the end), so short items keep both warpgroups busy too.
 //
 // Warps: 0-3 softmax of slot 0, 4-7 softmax of slot 1, 8 issues the products,
-// 9 loads (TMA), 10 schedules; 11 only completes the warpgroup whose registers
-// the softmax warps take over (a softmax thread holds a whole row of a tile,
-// 128 logits).  Tensor memory: S0 | S1 | O0 | O1, 128 columns each; the weights
+// 9 loads (TMA), 10 schedules, 11 looks over the V tiles that are masked for
+// some rows.  These four need few registers; the softmax warps take the rest
+// (a softmax thread holds a whole row of a tile, 128 logits).  Tensor memory: S0 | S1 | O0 | O1, 128 columns each; the weights
 // P (bf16) overwrite the first half of their S columns and are read from there
 // as the A operand of the second product.
 //
@@ -68,6 +68,11 @@ constexpr float kLazy = 32.0f;
 constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
 constexpr uint32_t kFullMask = 0xffffffffu;
 
+// Masked tiles of an item: its new tokens' rows (1024 at most for a tree, 256
+// for a prompt) and a ragged end on either side.  A list entry is the tile and
+// a bit for each of its 128 rows; entry 0 holds the count.
+constexpr int kMaxMasked = 10, kBadBytes = 4 + 20 * kMaxMasked;
+
 template <int D>
 struct Lay {
     static constexpr int kAtoms = D / 64;
@@ -81,10 +86,11 @@ struct Lay {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kOperand;
     static constexpr int kBar = kRing + kStages * kOperand;
-    static constexpr int kNumBars = 2 * kStages + 23;
+    static constexpr int kNumBars = 2 * kStages + 37;
     static constexpr int kMisc = kBar + kNumBars * 8;       // TMEM base, abort flag
     static constexpr int kSeg = (kMisc + 8 + 15) / 16 * 16; // two segment descriptions
-    static constexpr int kState = kSeg + 2 * 64;            // the slots' m and l [2 slots][2][128]
+    static constexpr int kBad = kSeg + 2 * 64;              // two lists of V rows taken out of the product
+    static constexpr int kState = kBad + 2 * kBadBytes;     // the slots' m and l [2 slots][2][128]
     static constexpr int kBytes = kState + 2048;
     static_assert(kBar % 8 == 0, "mbarrier alignment");
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -265,6 +271,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 struct Params {
     const int32_t *q_begin, *ctx_len;
     const uint32_t *mask;   // nullptr: causal
+    const uint16_t *Q, *K, *V;  // (read here only for rows that are not finite; else by TMA)
     uint16_t *out;
     float *part;            // shares: two states per CTA; nullptr: the counter deals whole items out
     int32_t *joins;         // shares: what to join, 8 words an entry (first CTA or -1, CTAs, token, head, rows)
@@ -295,7 +302,7 @@ enum SegField {
     kTiles,      // tiles
     kTiles0,     // tiles of slot 0
     kTiles1,     // tiles of slot 1
-    kTail,       // rows of the last tile below the length, if not all are (else 0)
+    kMaskLo,     // tiles that reach past this cache row hold rows that some token does not see
     kPart,       // state to write, -1: the result itself
     kSegFields
 };
@@ -438,7 +445,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(L::kStages + s); };
     constexpr int kB = 2 * L::kStages;
-    const uint32_t q_full = bar(kB), q_empty = bar(kB + 1), drain = bar(kB + 3);
+    const uint32_t q_full = bar(kB), q_empty = bar(kB + 1), loaded = bar(kB + 2), drain = bar(kB + 3);
     const uint32_t o_free = bar(kB + 4);
     auto seg_full = [&](int i) { return bar(kB + 5 + i); };
     auto seg_empty = [&](int i) { return bar(kB + 7 + i); };
@@ -446,9 +453,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     auto s_full = [&](int s) { return bar(kB + 11 + s); };
     auto p_full = [&](int s, int half) { return bar(kB + 13 + 2 * s + half); };  // keys 0..63, 64..127
     auto o_done = [&](int s) { return bar(kB + 17 + s); };
-    const uint32_t loaded = bar(kB + 20);
-    auto s_read = [&](int s) { return bar(kB + 21 + s); };
-    auto tail_done = [&](int i) { return bar(i ? kB + 19 : kB + 2); };
+    auto s_read = [&](int s) { return bar(kB + 19 + s); };
+    auto v_loading = [&](int m) { return bar(kB + 21 + (m & 7)); };
+    auto v_clean = [&](int m) { return bar(kB + 29 + (m & 7)); };
     auto seg = [&](int i) { return reinterpret_cast<volatile int *>(sm + L::kSeg + i * 64); };
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFullMask, tid >> 5, 0);
@@ -466,13 +473,16 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         mbar_init(state_empty, 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(seg_full(s), 1);
-            mbar_init(seg_empty(s), 10);
-            mbar_init(tail_done(s), 1);
+            mbar_init(seg_empty(s), 11);
             mbar_init(s_full(s), 1);
             mbar_init(s_read(s), 4);
             mbar_init(p_full(s, 0), 4);
             mbar_init(p_full(s, 1), 4);
             mbar_init(o_done(s), 1);
+        }
+        for (int m = 0; m < 8; ++m) {
+            mbar_init(v_loading(m), 1);
+            mbar_init(v_clean(m), 1);
         }
         misc[1] = 0;
         fence_mbar_init();
@@ -536,7 +546,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     // in pairs slot 0's rows, the earlier tokens, may end a tile or two before slot 1's
                     f[kTiles0] = pair ? max(0, min(last, tiles_upto(p, q, tok0 + tps - 1)) - first) : (nt + 1) / 2;
                     f[kTiles1] = pair ? nt : nt / 2;
-                    f[kTail] = nt > 0 && last * kTile > q.T ? q.T - (last - 1) * kTile : 0;
+                    f[kMaskLo] = p.mask ? q.T - q.n : q.T - q.n + tok0 + 1;
                     f[kPart] = part;
                     mbar_arrive(seg_full(k & 1));
                 }
@@ -681,7 +691,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // Ring order = the order in which the products use the tiles: K0
             // V0 K1 V1 .. in pairs, K0 K1 V0 K2 V1 .. for every other tile, and
             // one more K ahead where the next S does not wait for P.
-            int stage = 0, issued = 0, tails = 0, queries = 0, k = 0;
+            int stage = 0, issued = 0, masked = 0, queries = 0, k = 0;
             uint32_t parity = 1;  // of a stage's previous release (passes at once in the first round)
             bool ok = true;
             for (;; ++k) {
@@ -690,7 +700,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 volatile const int *f = seg(k & 1);
                 if (f[kEnd]) break;
                 const bool pair = f[kPair];
-                const int nt = f[kTiles], row0 = f[kRowBase] + f[kFirst] * kTile, tail = f[kTail];
+                const int nt = f[kTiles], row0 = f[kRowBase] + f[kFirst] * kTile;
+                const int mask_lo = f[kMaskLo] - f[kFirst] * kTile;  // within the segment's rows
                 if (k > 0) ok = wait_warp(q_empty, (k - 1) & 1, abort_flag, p.flags);
                 if (!ok) break;
                 if (lane == 0) {
@@ -724,27 +735,13 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int t = 0; t <= ahead && t < nt; ++t) load(true, t);
                 for (int t = 0; t < nt && ok; ++t) {
                     load(false, t);
+                    if (ok && (t + 1) * kTile > mask_lo) {
+                        if (lane == 0) mbar_arrive(v_loading(masked));
+                        ++masked;
+                    }
                     if (t + ahead + 1 < nt) load(true, t + ahead + 1);
                 }
                 if (!ok) break;
-                if (tail > 0) {
-                    // the last V tile (the item just loaded) reaches past the
-                    // length: cache rows there may hold anything, NaN included,
-                    // and 0 * NaN must not reach the sums
-                    const int s = stage == 0 ? L::kStages - 1 : stage - 1;
-                    ok = wait_warp(full(s), ((issued - 1) / L::kStages) & 1, abort_flag, p.flags);
-                    if (!ok) break;
-                    uint8_t *v = sm + L::kRing + s * L::kOperand;
-#pragma unroll
-                    for (int a = 0; a < L::kAtoms; ++a)
-                        for (int o = tail * 128 + lane * 16; o < kTile * 128; o += 512)
-                            *reinterpret_cast<uint4 *>(v + a * 16384 + o) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    // (two barriers in turn: this warp may be a segment ahead of the products)
-                    if (lane == 0) mbar_arrive(tail_done(tails & 1));
-                    ++tails;
-                }
                 if (lane == 0) {
                     mbar_arrive(loaded);
                     mbar_arrive(seg_empty(k & 1));
@@ -755,6 +752,82 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (queries > 0) mbar_wait_bounded(q_full, (queries - 1) & 1, p.flags);
             for (int i = max(0, issued - L::kStages); i < issued; ++i)
                 mbar_wait_bounded(full(i % L::kStages), (i / L::kStages) & 1, p.flags);
+        } else if (warp == 11) {
+            // ======================================================== masked tiles
+            // V tiles with rows that not every token of the item sees, before
+            // the product with P uses them: a weight of 0 for such a row does
+            // not keep a NaN or an infinity in it out of the sums.  Rows at and
+            // past the length, which may hold anything, are cleared; so are
+            // rows with a value that is not finite, and listed: the epilogue
+            // adds those to the tokens that see them.
+            int masked = 0, ring = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                ok = wait_warp(seg_full(k & 1), (k >> 1) & 1, abort_flag, p.flags);
+                if (!ok) break;
+                volatile const int *f = seg(k & 1);
+                if (f[kEnd]) break;
+                const int nt = f[kTiles], ahead = (f[kPair] ? 0 : 1) + (L::kSepP ? 1 : 0);
+                const int row0 = f[kFirst] * kTile, mask_lo = f[kMaskLo] - row0, len = f[kLen] - row0;
+                volatile int *bad = reinterpret_cast<volatile int *>(sm + L::kBad + (k & 1) * kBadBytes);
+                if (lane == 0) bad[0] = 0;
+                __syncwarp();
+                int n_bad = 0;
+                for (int t = max(0, mask_lo / kTile); t < nt && ok; ++t) {
+                    if ((t + 1) * kTile <= mask_lo) continue;
+                    // once the load is issued the barrier is in this tile's phase
+                    ok = wait_warp(v_loading(masked), (masked >> 3) & 1, abort_flag, p.flags);
+                    const int item = ring + min(nt, t + ahead + 1) + t;
+                    if (ok) ok = wait_warp(full(item % L::kStages), (item / L::kStages) & 1, abort_flag, p.flags);
+                    if (!ok) break;
+                    uint8_t *v = sm + L::kRing + (item % L::kStages) * L::kOperand;
+                    const int r0 = max(0, mask_lo - t * kTile), r1 = max(r0, min(kTile, len - t * kTile));
+                    bool wrote = r1 < kTile;
+#pragma unroll
+                    for (int a = 0; a < L::kAtoms; ++a)
+                        for (int o = r1 * 128 + lane * 16; o < kTile * 128; o += 512)
+                            *reinterpret_cast<uint4 *>(v + a * 16384 + o) = make_uint4(0, 0, 0, 0);
+                    uint32_t top = 0u;  // the largest magnitudes, as pairs of 16-bit integers
+#pragma unroll
+                    for (int a = 0; a < L::kAtoms; ++a)
+#pragma unroll 4
+                        for (int o = r0 * 128 + lane * 16; o < r1 * 128; o += 512) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(v + a * 16384 + o);
+                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                        }
+                    if (__any_sync(kFullMask, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+                        // which rows: lane by lane
+                        if (lane == 0 && n_bad < kMaxMasked) bad[1 + 5 * n_bad] = row0 + t * kTile;
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = q * 32 + lane;
+                            bool odd = false;
+                            if (r >= r0 && r < r1)
+                                for (int a = 0; a < L::kAtoms; ++a)
+                                    for (int o = 0; o < 128; o += 4) {
+                                        const uint32_t x = *reinterpret_cast<const uint32_t *>(v + a * 16384 + r * 128 + o);
+                                        odd |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+                                    }
+                            if (odd)
+                                for (int a = 0; a < L::kAtoms; ++a)
+                                    for (int o = 0; o < 128; o += 16)
+                                        *reinterpret_cast<uint4 *>(v + a * 16384 + r * 128 + o) = make_uint4(0, 0, 0, 0);
+                            const uint32_t w = __ballot_sync(kFullMask, odd);
+                            if (lane == 0 && n_bad < kMaxMasked) bad[2 + 5 * n_bad + q] = (int)w;
+                        }
+                        n_bad = min(n_bad + 1, kMaxMasked);
+                        if (lane == 0) bad[0] = n_bad;
+                        wrote = true;
+                    }
+                    if (wrote) fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_clean(masked));
+                    ++masked;
+                }
+                ring += 2 * nt;
+                if (lane == 0) mbar_arrive(seg_empty(k & 1));
+                __syncwarp();
+            }
         } else if (warp == 8) {
             // ======================================================== products
             // One thread issues all of them.  Per slot the order is S(0), then
@@ -770,7 +843,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const uint32_t q_lo = (uint32_t)kd, hi = (uint32_t)(kd >> 32);
                 const uint32_t k_lo = q_lo + (L::kRing >> 4), v_lo = (uint32_t)vd;
                 int k_stage = 0, v_stage = 0, next = 0;
-                uint32_t next_parity = 0, tails = 0;
+                uint32_t next_parity = 0;
+                int masked = 0;
                 uint32_t done = 0, read = 0;  // bit s = parity of slot s's tiles so far (P used, S read)
                 bool ok = true;
                 auto acquire = [&](int &st) {
@@ -787,7 +861,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     volatile const int *f = seg(k & 1);
                     if (f[kEnd]) break;
                     const bool pair = f[kPair];
-                    const int nt = f[kTiles], nt0 = f[kTiles0], nt1 = f[kTiles1], tail = f[kTail];
+                    const int nt = f[kTiles], nt0 = f[kTiles0], nt1 = f[kTiles1];
+                    const int mask_lo = f[kMaskLo] - f[kFirst] * kTile;
                     ok = wait_role(q_full, k & 1, abort_flag, p.flags);
                     // round j: slot 0's and slot 1's step, each the PV of its
                     // tile j and the S of its tile j + 1.  In pairs both use
@@ -828,9 +903,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         if (!ok || tile >= nt) return;
                         if (!pair || slot == 0) {
                             acquire(v_stage);
-                            if (tail > 0 && tile + 1 == nt && ok) {
-                                ok = wait_role(tail_done(tails & 1), (tails >> 1) & 1u, abort_flag, p.flags);
-                                ++tails;
+                            if ((tile + 1) * kTile > mask_lo) {  // looked over by warp 11
+                                if (ok) ok = wait_role(v_clean(masked), (masked >> 3) & 1, abort_flag, p.flags);
+                                ++masked;
                             }
                             // the previous segment's sums have been read
                             if (slot == 0 && j == 0 && k > 0 && ok) ok = wait_role(o_free, (k - 1) & 1, abort_flag, p.flags);
@@ -1100,6 +1175,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const int h = f[kHead] + (row & ((1 << p.g_shift) - 1));
             uint16_t *dst = p.out + ((size_t)(f[kTok] + ti) * p.Hq + h) * D;
             float *part = p.part + (size_t)max(part_slot, 0) * ((D + 2) * kItemRows) + (pair ? slot : 0) * kSlotRows + row;
+            volatile const int *bad = reinterpret_cast<volatile const int *>(sm + L::kBad + (k & 1) * kBadBytes);
+            const int n_bad = bad[0];
             const int q0 = pair ? 0 : slot * (D / 32), q1 = pair ? D / 16 : q0 + D / 32;  // groups of 16 head dims
 #pragma unroll 1
             for (int q = q0; q < q1; ++q) {
@@ -1123,6 +1200,25 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 if (empty_row) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                }
+                // V rows that warp 11 took out (none, as a rule): p v for those this row sees
+#pragma unroll 1
+                for (int e = 0; e < n_bad; ++e) {
+                    const int r0 = bad[1 + 5 * e];
+#pragma unroll 1
+                    for (int j = 0; j < kTile; ++j) {
+                        if (!((bad[2 + 5 * e + (j >> 5)] >> (j & 31)) & 1) || !(allowed(r0 + j) & 1u)) continue;
+                        const size_t kv = ((size_t)f[kRowBase] + r0 + j) * D;
+                        const uint16_t *qr = p.Q + (dst - p.out);
+                        float x = 0.f;
+#pragma unroll 1
+                        for (int i = 0; i < D; ++i)
+                            x = fmaf(__uint_as_float((uint32_t)qr[i] << 16), __uint_as_float((uint32_t)p.K[kv + i] << 16), x);
+                        x = ex2(fmaf(x, p.c, -m)) * (part_slot < 0 ? 1.f / l : 1.f);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = fmaf(x, __uint_as_float((uint32_t)p.V[kv + q * 16 + i] << 16), o[i]);
+                    }
                 }
                 if (part_slot < 0) {
                     if (store) {
@@ -1330,6 +1426,9 @@ cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_
     p.q_begin = q_begin;
     p.ctx_len = ctx_len;
     p.mask = mask;
+    p.Q = Q;
+    p.K = K;
+    p.V = V;
     p.out = out;
     p.flags = reinterpret_cast<uint32_t *>(w);
     p.counter = reinterpret_cast<uint32_t *>(w + 64);

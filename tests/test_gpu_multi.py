@@ -592,3 +592,83 @@ def test_calls_on_a_side_stream_wait_for_it_only():
         tb.prompt_attn(dm, Q2, K, V, i32(starts(n)), 64, i32(T), scale, got, ws, stream=side)
     side.synchronize()
     assert torch.equal(got, out)
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("n,T", [([40], [40]), ([150, 20], [700, 20]), ([60], [9000])])
+def test_non_finite_rows_reach_only_the_tokens_that_see_them(n, T, tree, d):
+    """A NaN or an infinity in a new token's K or V row changes the tokens that
+    attend to it, and no other."""
+    hq, hkv = 8, 2
+    g = torch.Generator(device=DEV).manual_seed(21)
+    r = np.random.RandomState(21)
+    cap = (max(T) + 127) // 128 * 128
+    K, V = make_cache(g, len(n), hkv, cap, d, T)
+    Q = torch.randn(sum(n), hq, d, generator=g, device=DEV).to(torch.bfloat16)
+    Kc, Vc = K.clone(), V.clone()
+    at = {}                                   # (sequence, new token) -> what is odd about its row
+    for b in range(len(n)):
+        for j, kind in ((n[b] // 3, "V nan"), (n[b] // 2, "V inf"), (n[b] - 2, "K nan"), (n[b] - 1, "V nan")):
+            row = T[b] - n[b] + j
+            at[b, j] = kind
+            if kind == "K nan":
+                K[b, :, row, 5] = float("nan")
+                Kc[b, :, row] = 0
+            else:
+                V[b, :, row, 7] = float("nan") if kind == "V nan" else float("inf")
+                Vc[b, :, row, 7] = 0
+    masks = [random_tree(k, r) if tree else np.tril(np.ones((k, k), dtype=bool)) for k in n]
+    if tree:
+        for m in masks:                       # the first odd row is no ancestor of most
+            m[m.shape[0] // 3 + 2:, m.shape[0] // 3] = False
+    out = torch.zeros_like(Q)
+    dm, scale = tb.dims(len(n), hq, hkv, d, 16, cap), 1 / math.sqrt(d)
+    size = tb.tree_attn_workspace_bytes if tree else tb.prompt_attn_workspace_bytes
+    ws = tb.workspace(size(dm, sum(n), max(n)))
+    if tree:
+        mask = pack_rows([row for m in masks for row in m], (max(n) + 31) // 32)
+        mask = mask if mask.shape[1] else None
+        tb.tree_attn(dm, Q, K, V, i32(starts(n)), max(n), i32(T), mask, scale, out, ws)
+    else:
+        tb.prompt_attn(dm, Q, K, V, i32(starts(n)), max(n), i32(T), scale, out, ws)
+    assert tb.workspace_check(ws) == 0
+    ref, tol = reference(Q, Kc, Vc, n, T, scale, tree_see(masks, n, T))
+    s = starts(n)
+    clean = 0
+    for b in range(len(n)):
+        for i in range(n[b]):
+            seen = {kind for (bb, j), kind in at.items() if bb == b and masks[b][i, j]}
+            o, x = out[s[b] + i], slice(s[b] + i, s[b] + i + 1)
+            if "K nan" in seen:
+                assert o.isnan().all(), (b, i)
+                continue
+            if "V nan" in seen:
+                assert o[:, 7].isnan().all(), (b, i)
+            elif "V inf" in seen:
+                assert (o[:, 7] == float("inf")).all(), (b, i)
+            keep = [c for c in range(d) if c != 7 or not seen]
+            check(out[x][..., keep], ref[x][..., keep], tol[x][..., keep], f"token {b, i}")
+            clean += not seen
+    assert clean >= sum(n) // 4
+
+
+def test_prompt_logits_far_apart():
+    """Logits that rise by hundreds along the context (the running reference
+    is raised again and again), and ones that fall by as much."""
+    n, T, d = [130, 70], [900, 2000], 128
+    g = torch.Generator(device=DEV).manual_seed(31)
+    K, V = make_cache(g, 2, 2, 2048, d, T, heavy=False)
+    Q = torch.randn(200, 8, d, generator=g, device=DEV).to(torch.bfloat16)
+    u = torch.randn(d, generator=g, device=DEV)
+    Q = (Q.float() * 0.1 + u).to(torch.bfloat16)
+    for sign in (1, -1):
+        ramp = sign * torch.linspace(-4, 4, 2048, device=DEV)[None, None, :, None]
+        Kr = (K.float() * 0.1 + ramp * u).to(torch.bfloat16)
+        for b in range(2):
+            Kr[b, :, T[b]:] = float("nan")
+        _, _, _, out, scale = run_prompt(n, T, 8, 2, d, extra=0, K=Kr, V=V, Q=Q, cap=2048)
+        ref, tol = reference(Q, Kr, V, n, T, scale, causal(n, T))
+        check(out, ref, tol, f"sign {sign}")
