@@ -329,50 +329,28 @@ def kv_append(d: TbDims, n_layers: int, src, caches, ctx_len, ws, stream=None):
                                _bytes(ws), _stream(stream)))
 
 
-# The calls that take several new tokens of a sequence at once check what the C
-# side cannot see: types, shapes against dims, and that every tensor is on the
-# workspace's device, which is made current for the call (without a stream
-# argument they run on that device's current stream).  They are called once per
-# layer of a step of a few microseconds, so the checks are kept to plain
-# comparisons and the message is put together only once one has failed.
+# The calls that take several new tokens of a sequence at once run once per layer
+# of a step of a few microseconds.  Their tensors' types, shapes, devices and
+# layouts are checked, and the workspace's device is made current for the call,
+# by _tbcall (csrc/tbcall.cpp), which then calls the entry point; without a
+# stream argument they run on that device's current stream.
 
-_BF16, _I32 = torch.bfloat16, torch.int32
-
-
-def _misfit(name, t, dtype, shape, dev):
-    """Raise for the first thing wrong with tensor `t` (there is one)."""
-    if not t.is_cuda:
-        raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes device tensors")
-    if t.dtype is not dtype:
-        raise TbError(TB_ERR_INVALID_ARG, f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise TbError(TB_ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.get_device() != dev:
-        raise TbError(TB_ERR_INVALID_ARG, f"{name} is on {t.device}, the workspace on cuda:{dev}")
-    raise TbError(TB_ERR_INVALID_ARG, f"{name}: libtb takes contiguous tensors")
+_call = None
 
 
-def _at(name, t, dtype, shape, dev):
-    """Address of a contiguous device tensor of that type and shape."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous() or dev < 0:
-        _misfit(name, t, dtype, shape, dev)
-    return t.data_ptr()
-
-
-def _call_on(dev: int, stream, fn, *args):
-    """fn(*args, stream) with device `dev` current."""
-    if torch._C._cuda_getDevice() != dev:
-        with torch.cuda.device(dev):
-            return _call_on(dev, stream, fn, *args)
-    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    if st != TB_OK:
-        _check(st)
-
-
-def _host_only(*tensors):
-    for t in tensors:
-        if not t.is_cuda:
-            raise TbError(TB_ERR_INVALID_ARG, "libtb takes device tensors")
+def _tbcall():
+    global _call
+    if _call is None:
+        lib = load()
+        try:
+            from . import _tbcall as mod
+        except ImportError as e:
+            raise TbError(-1, f"_tbcall.so is missing or does not load ({e}): build it with "
+                              "`python -m query_aware_sparse_tb_b200.build`") from e
+        mod.bind(TbError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.tb_norm_rope_append, lib.tb_prompt_attn, lib.tb_tree_attn, lib.tb_tree_accept)))
+        _call = mod
+    return _call
 
 
 def norm_rope_append(d: TbDims, qkv, q_begin, ctx_len, pos, q_weight, k_weight, eps: float, inv_freq,
@@ -381,34 +359,10 @@ def norm_rope_append(d: TbDims, qkv, q_begin, ctx_len, pos, q_weight, k_weight, 
     further apart); pos [n_tokens] int32 or None (the cache row); q_weight and
     k_weight [d] bf16 or None; inv_freq [rot_dim / 2] float64 or None; writes Q
     [n_tokens][Hq][d] and the new rows of the caches K and V."""
-    dev, B, hq, hkv, hd = ws.get_device(), d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim
-    n, width, cache = Q.shape[0], (hq + 2 * hkv) * hd, (B, hkv, d.ctx_cap, hd)
-    stride, inner = qkv.stride() if qkv.dim() == 2 else (0, 0)
-    if dev < 0 or qkv.get_device() != dev or qkv.dtype is not _BF16 or qkv.shape != (n, width) or inner != 1:
-        _host_only(ws, qkv)
-        raise TbError(TB_ERR_INVALID_ARG, f"qkv: expected bfloat16 [{n}][{width}] on cuda:{dev} with contiguous rows")
-    _call_on(dev, stream, (_lib or load()).tb_norm_rope_append, ctypes.byref(d), qkv.data_ptr(),
-             stride if n > 1 else max(width, stride), _at("q_begin", q_begin, _I32, (B + 1,), dev), n,
-             _at("ctx_len", ctx_len, _I32, (B,), dev), None if pos is None else _at("pos", pos, _I32, (n,), dev),
-             None if q_weight is None else _at("q_weight", q_weight, _BF16, (hd,), dev),
-             None if k_weight is None else _at("k_weight", k_weight, _BF16, (hd,), dev), eps,
-             None if inv_freq is None else _at("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev),
-             0 if inv_freq is None else 2 * inv_freq.numel(), TB_ROPE_INTERLEAVED if interleaved else TB_ROPE_HALF,
-             _at("Q", Q, _BF16, (n, hq, hd), dev), _at("K", K, _BF16, cache, dev), _at("V", V, _BF16, cache, dev),
-             ws.data_ptr(), ws.nbytes)
-
-
-def _multi_attn(fn, d: TbDims, Q, K, V, q_begin, max_new, ctx_len, mask, scale, out, ws, stream):
-    dev, B, hq, hd = ws.get_device(), d.batch, d.n_q_heads, d.head_dim
-    n = Q.shape[0]
-    rows, cache = (n, hq, hd), (B, d.n_kv_heads, d.ctx_cap, hd)
-    args = (ctypes.byref(d), _at("Q", Q, _BF16, rows, dev), _at("K", K, _BF16, cache, dev),
-            _at("V", V, _BF16, cache, dev), _at("q_begin", q_begin, _I32, (B + 1,), dev), n, max_new,
-            _at("ctx_len", ctx_len, _I32, (B,), dev))
-    if mask is not None:
-        words = mask.dtype if mask.dtype is torch.uint32 else _I32
-        args += (_at("mask", mask, words, (n, (max_new + 31) // 32), dev),)
-    _call_on(dev, stream, fn, *args, scale, _at("out", out, _BF16, rows, dev), ws.data_ptr(), ws.nbytes)
+    st = (_call or _tbcall()).norm_rope_append(d, qkv, q_begin, ctx_len, pos, q_weight, k_weight, eps, inv_freq,
+                                               interleaved, Q, K, V, ws, stream)
+    if st:
+        _check(st)
 
 
 def prompt_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
@@ -419,7 +373,9 @@ def prompt_attn(d: TbDims, Q, K, V, q_begin, max_new: int, ctx_len, scale: float
     """tb_prompt_attn: causal attention of packed prompts over the caches;
     Q and out [n_tokens][Hq][d] bf16, q_begin [batch + 1] int32, max_new an
     upper bound on a sequence's new tokens."""
-    _multi_attn((_lib or load()).tb_prompt_attn, d, Q, K, V, q_begin, max_new, ctx_len, None, scale, out, ws, stream)
+    st = (_call or _tbcall()).prompt_attn(d, Q, K, V, q_begin, max_new, ctx_len, scale, out, ws, stream)
+    if st:
+        _check(st)
 
 
 def tree_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
@@ -429,20 +385,17 @@ def tree_attn_workspace_bytes(d: TbDims, n_tokens: int, max_new: int) -> int:
 def tree_attn(d: TbDims, Q, K, V, q_begin, max_new: int, ctx_len, mask, scale: float, out, ws, stream=None):
     """tb_tree_attn: as prompt_attn, with the drafted tokens' attention bits
     mask [n_tokens][ceil(max_new / 32)] (int32 or uint32 words)."""
-    if mask is None:
-        raise TbError(TB_ERR_INVALID_ARG, "tree_attn needs a mask")
-    _multi_attn((_lib or load()).tb_tree_attn, d, Q, K, V, q_begin, max_new, ctx_len, mask, scale, out, ws, stream)
+    st = (_call or _tbcall()).tree_attn(d, Q, K, V, q_begin, max_new, ctx_len, mask, scale, out, ws, stream)
+    if st:
+        _check(st)
 
 
 def tree_accept(d: TbDims, n_layers: int, caches, q_begin, ctx_len, path, path_len, new_len, ws, stream=None):
     """tb_tree_accept: caches as for kv_append; path [batch][path_cap] int32,
     path_len and new_len [batch] int32."""
-    dev, B, cap = ws.get_device(), d.batch, path.shape[-1]
-    _call_on(dev, stream, (_lib or load()).tb_tree_accept, ctypes.byref(d), n_layers,
-             _at("caches", caches, torch.int64, (2 * n_layers,), dev), _at("q_begin", q_begin, _I32, (B + 1,), dev),
-             _at("ctx_len", ctx_len, _I32, (B,), dev), _at("path", path, _I32, (B, cap), dev), cap,
-             _at("path_len", path_len, _I32, (B,), dev), _at("new_len", new_len, _I32, (B,), dev), ws.data_ptr(),
-             ws.nbytes)
+    st = (_call or _tbcall()).tree_accept(d, n_layers, caches, q_begin, ctx_len, path, path_len, new_len, ws, stream)
+    if st:
+        _check(st)
 
 
 def selftest_bounded_wait(ws, budget_cycles: int, stream=None):

@@ -1,4 +1,5 @@
-"""Build libtb.so in-tree with nvcc for sm_100a.
+"""Build libtb.so in-tree with nvcc for sm_100a, and _tbcall.so (the Python
+side's argument marshalling, host code only) with g++.
 
     python -m query_aware_sparse_tb_b200.build
 
@@ -9,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
 import sys
 
@@ -17,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtb.so")
+CALL = os.path.join(PKG, "_tbcall.so")
 SOURCES = ["api.cu", "attn.cu", "select.cu", "select_cluster.cu", "gemm_tc.cu", "noalloc.cu", "kv.cu",
            "multi_attn.cu", "rope.cu", "tree.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -52,7 +55,32 @@ def build(force: bool = False, verbose: bool = False) -> str:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    build_call(force)
     return LIB
+
+
+def build_call(force: bool = False) -> str:
+    """_tbcall.so: a CPython module over torch's C++ headers."""
+    src = os.path.join(CSRC, "tbcall.cpp")
+    if force or not _newer(CALL, [src, os.path.join(ROOT, "include", "tb.h")]):
+        import sysconfig
+
+        import torch
+        base = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
+        tmp = f"{CALL}.{os.getpid()}.tmp"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-isystem", os.path.join(base, "include"),
+               "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+               src, "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+               f"-Wl,-rpath,{os.path.join(base, 'lib')}"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, CALL)
+    return CALL
 
 
 if __name__ == "__main__":

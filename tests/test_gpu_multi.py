@@ -672,3 +672,69 @@ def test_prompt_logits_far_apart():
         _, _, _, out, scale = run_prompt(n, T, 8, 2, d, extra=0, K=Kr, V=V, Q=Q, cap=2048)
         ref, tol = reference(Q, Kr, V, n, T, scale, causal(n, T))
         check(out, ref, tol, f"sign {sign}")
+
+
+# ------------------------------------------------------------------ what the binding refuses
+
+def test_binding_refuses_types_shapes_and_layouts():
+    d = tb.dims(2, 8, 2, 64, 16, 32)
+    z = lambda *s, t=torch.bfloat16, dev=DEV: torch.zeros(*s, dtype=t, device=dev)  # noqa: E731
+    good = dict(Q=z(3, 8, 64), K=z(2, 2, 32, 64), V=z(2, 2, 32, 64), q_begin=i32([0, 1, 3]), ctx_len=i32([1, 2]),
+                out=z(3, 8, 64), mask=z(3, 1, t=torch.int32), ws=tb.workspace(1 << 22), qkv=z(3, 12 * 64),
+                inv=torch.ones(32, dtype=F64, device=DEV), pos=i32([0, 1, 2]), w=z(64), caches=z(2, t=torch.int64),
+                path=z(2, 4, t=torch.int32), plen=i32([0, 0]), new=i32([0, 0]))
+
+    def prompt(**kw):
+        a = {**good, **kw}
+        tb.prompt_attn(d, a["Q"], a["K"], a["V"], a["q_begin"], kw.get("mx", 2), a["ctx_len"], kw.get("scale", 0.1),
+                       a["out"], a["ws"])
+
+    def tree(**kw):
+        a = {**good, **kw}
+        tb.tree_attn(d, a["Q"], a["K"], a["V"], a["q_begin"], 2, a["ctx_len"], a["mask"], 0.1, a["out"], a["ws"])
+
+    def rope(**kw):
+        a = {**good, **kw}
+        tb.norm_rope_append(d, a["qkv"], a["q_begin"], a["ctx_len"], a["pos"], a["w"], a["w"], 1e-6, a["inv"], False,
+                            a["Q"], a["K"], a["V"], a["ws"])
+
+    def accept(**kw):
+        a = {**good, **kw}
+        tb.tree_accept(d, 1, a["caches"], a["q_begin"], a["ctx_len"], a["path"], a["plen"], a["new"], a["ws"])
+
+    for call, odd in [
+        (prompt, dict(Q=z(3, 8, 64, t=torch.float16))), (prompt, dict(Q=z(3, 4, 64))), (prompt, dict(Q=z(3, 512))),
+        (prompt, dict(K=z(2, 2, 31, 64))), (prompt, dict(V=z(2, 2, 64, 32).transpose(2, 3))),
+        (prompt, dict(q_begin=i32([0, 3]))), (prompt, dict(q_begin=i32([0, 1, 3]).long())),
+        (prompt, dict(ctx_len=i32([1, 2]).cpu())), (prompt, dict(out=z(4, 8, 64))), (prompt, dict(out=z(3, 8, 64, t=torch.float32))),
+        (prompt, dict(out=good["Q"])), (prompt, dict(mx=0)), (prompt, dict(mx=1 << 40)), (prompt, dict(scale=0.0)),
+        (prompt, dict(ws=tb.workspace(1 << 22).cpu())), (prompt, dict(Q="no tensor")),
+        (tree, dict(mask=z(3, 2, t=torch.int32))), (tree, dict(mask=z(3, 1, t=torch.int64))), (tree, dict(mask=None)),
+        (rope, dict(qkv=z(3, 11 * 64))), (rope, dict(qkv=z(12 * 64, 3).t())), (rope, dict(qkv=z(3, 12 * 64, t=torch.float32))),
+        (rope, dict(pos=i32([0, 1]))), (rope, dict(w=z(32))), (rope, dict(inv=torch.ones(32, device=DEV))),
+        (rope, dict(inv=torch.ones(36, dtype=F64, device=DEV))), (rope, dict(K=z(2, 2, 32, 32))),
+        (accept, dict(caches=z(4, t=torch.int64))), (accept, dict(path=z(4, t=torch.int32))),
+        (accept, dict(new=good["ctx_len"])), (accept, dict(plen=i32([0]))),
+    ]:
+        with pytest.raises(tb.TbError):
+            call(**odd)
+    prompt(), tree(), rope(), accept()         # and takes what is right
+    with pytest.raises(TypeError):
+        tb.prompt_attn(d, good["Q"], good["K"], good["V"], good["q_begin"], 2, good["ctx_len"], "0.1", good["out"], good["ws"])
+    torch.cuda.synchronize()
+    assert tb.workspace_check(good["ws"]) in (0, _lib.TB_FLAG_BAD_CACHE)   # (accept's cache addresses are null)
+
+
+def test_calls_of_no_tokens_do_nothing():
+    d = tb.dims(2, 8, 2, 64, 16, 32)
+    K = torch.randn(2, 2, 32, 64, device=DEV).to(torch.bfloat16)
+    V, want = K.clone(), K.clone()
+    Q = torch.zeros(0, 8, 64, dtype=torch.bfloat16, device=DEV)
+    ws = tb.workspace(tb.prompt_attn_workspace_bytes(d, 0, 1))
+    qb, ctx = i32([0, 0, 0]), i32([0, 0])
+    tb.prompt_attn(d, Q, K, V, qb, 1, ctx, 0.1, torch.zeros_like(Q), ws)
+    tb.tree_attn(d, Q, K, V, qb, 1, ctx, torch.zeros(0, 1, dtype=torch.int32, device=DEV), 0.1, torch.zeros_like(Q), ws)
+    tb.norm_rope_append(d, torch.zeros(0, 12 * 64, dtype=torch.bfloat16, device=DEV), qb, ctx, None, None, None, 0.0, None,
+                        False, Q, K, V, ws)
+    torch.cuda.synchronize()
+    assert tb.workspace_check(ws) == 0 and torch.equal(K, want) and torch.equal(V, want)
