@@ -341,8 +341,10 @@ __device__ __forceinline__ int item_tiles(const Params &p, const Seq &q, int ite
     const int tpi = kItemRows >> p.g_shift;
     return tiles_upto(p, q, min((item + 1) * tpi, q.kept) - 1);
 }
+// Inclusive sum over the lanes' sequences (one sequence: that of lane 0).
 template <typename T>
-__device__ __forceinline__ T warp_prefix(T v, int lane) {  // inclusive
+__device__ __forceinline__ T warp_prefix(const Params &p, T v, int lane) {
+    if (p.batch == 1) return __shfl_sync(kFullMask, v, 0);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const T u = __shfl_up_sync(kFullMask, v, o);
@@ -357,7 +359,7 @@ __device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, Se
     int before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const Seq mine = load_seq(p, b0 + lane);
-        const int items = items_of(p, mine.kept), incl = warp_prefix(items, lane);
+        const int items = items_of(p, mine.kept), incl = warp_prefix(p, items, lane);
         const uint32_t hit = __ballot_sync(kFullMask, tau < before + incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
@@ -582,14 +584,14 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             } else {
                 const int cta = blockIdx.x;
                 const Seq seq0 = load_seq(p, lane);  // of the first 32 sequences
-                const long long units0 = warp_prefix(seq_units(p, seq0), lane);
-                const int items0 = warp_prefix(items_of(p, seq0.kept), lane);
+                const long long units0 = warp_prefix(p, seq_units(p, seq0), lane);
+                const int items0 = warp_prefix(p, items_of(p, seq0.kept), lane);
                 long long total = __shfl_sync(kFullMask, units0, 31);
                 int total_items = __shfl_sync(kFullMask, items0, 31);
                 for (int b0 = 32; b0 < p.batch; b0 += 32) {
                     const Seq mine = load_seq(p, b0 + lane);
-                    total += __shfl_sync(kFullMask, warp_prefix(seq_units(p, mine), lane), 31);
-                    total_items += __shfl_sync(kFullMask, warp_prefix(items_of(p, mine.kept), lane), 31);
+                    total += __shfl_sync(kFullMask, warp_prefix(p, seq_units(p, mine), lane), 31);
+                    total_items += __shfl_sync(kFullMask, warp_prefix(p, items_of(p, mine.kept), lane), 31);
                 }
                 total_items *= p.Hkv;
                 const Shares sh(total, gridDim.x);
@@ -609,8 +611,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 Seq q;
                 for (int b0 = 0; w < w1 && b0 < p.batch; b0 += 32) {
                     const Seq mine = b0 == 0 ? seq0 : load_seq(p, b0 + lane);
-                    const long long incl = b0 == 0 ? units0 : warp_prefix(seq_units(p, mine), lane);
-                    const int before = b0 == 0 ? items0 : warp_prefix(items_of(p, mine.kept), lane);
+                    const long long incl = b0 == 0 ? units0 : warp_prefix(p, seq_units(p, mine), lane);
+                    const int before = b0 == 0 ? items0 : warp_prefix(p, items_of(p, mine.kept), lane);
                     const uint32_t hit = __ballot_sync(kFullMask, w < at + incl);
                     if (hit) {
                         const int l = __ffs(hit) - 1;
@@ -657,7 +659,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int b0 = 0; b0 < p.batch; b0 += 32) {
                         bool odd = false;
                         const Seq mine = load_seq(p, b0 + lane);
-                        const int upto = before + warp_prefix(items_of(p, mine.kept), lane);
+                        const int upto = before + warp_prefix(p, items_of(p, mine.kept), lane);
                         before = __shfl_sync(kFullMask, upto, 31);
                         if (b0 + lane < p.batch) {
                             const Seq q = mine;
@@ -1263,42 +1265,45 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 // Joins the states of an item that was shared out:
 //   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
 // blockIdx.x is the entry, y a block of 32 rows (lane = row, so the states are
-// read 128 bytes at a time), z a block of 32 head dims, 8 per warp.  The loads
-// of 8 states are in flight at once: latency is all there is to it.  The tile
-// is turned in shared memory and stored row by row.
-template <int D>
-__global__ void __launch_bounds__(128)
+// read 128 bytes at a time), z a block of 32 head dims, 8 per warp.  Latency is
+// all there is to it: the loads of 8 states are in flight at once, and where an
+// item has many states (few items over a long context) SG = 4 groups of 4
+// warps take every fourth state each (a 64K tree's 19 states in one round
+// trip instead of three).
+template <int D, int SG>
+__global__ void __launch_bounds__(128 * SG)
 multi_join_kernel(const Params p) {
-    __shared__ float tile[32][33];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float tile[SG][32][33], ml[SG][2][32];
+    const int tid = threadIdx.x, lane = tid & 31, dg = (tid >> 5) & 3, sg = tid >> 7;
     griddep_wait();
     griddep_launch_dependents();
     const int4 e = *reinterpret_cast<const int4 *>(p.joins + 8 * blockIdx.x);
     const int rows = p.joins[8 * blockIdx.x + 4];
-    const int from = e.x, n = e.y, tok = e.z, head = e.w;  // CTAs from .. from + n - 1: state 2 c + 1 of the first, 2 c of the others
+    // CTAs from .. from + n - 1: state 2 c + 1 of the first, 2 c of the others
+    const int from = e.x, n = e.y, tok = e.z, head = e.w;
     if (from < 0 || (int)blockIdx.y * 32 >= rows) return;
     constexpr size_t kRec = (size_t)(D + 2) * kItemRows;
-    const int d0 = blockIdx.z * 32 + warp * 8;
+    const int d0 = blockIdx.z * 32 + dg * 8;
     const float *base = p.part + blockIdx.y * 32 + lane;
     float M = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     constexpr int kBatch = 8;
-    for (int s0 = 0; s0 < n; s0 += kBatch) {
+    for (int s0 = sg; s0 < n; s0 += SG * kBatch) {
         float ms[kBatch], ls[kBatch], v[kBatch][8];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
+            const int s = s0 + SG * u;
             ms[u] = -INFINITY;
             ls[u] = 0.f;
-            if (s0 + u < n) {
-                const float *r = base + (size_t)(2 * (from + s0 + u) + (s0 + u == 0)) * kRec;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+            if (s < n) {
+                const float *r = base + (size_t)(2 * (from + s) + (s == 0)) * kRec;
                 ms[u] = r[(size_t)D * kItemRows];
                 ls[u] = r[(size_t)(D + 1) * kItemRows];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[u][i] = r[(size_t)(d0 + i) * kItemRows];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
             }
         }
         float mn = M;
@@ -1317,14 +1322,34 @@ multi_join_kernel(const Params p) {
         }
         M = mn;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile[lane][warp * 8 + i] = acc[i] * inv;
+    for (int i = 0; i < 8; ++i) tile[sg][lane][dg * 8 + i] = acc[i];
+    if (dg == 0) {
+        ml[sg][0][lane] = M;
+        ml[sg][1][lane] = l;
+    }
     __syncthreads();
+    if (tid >= 128) return;
     const int r = tid >> 2, c8 = (tid & 3) * 8, rr = blockIdx.y * 32 + r;
     if (rr >= rows) return;
-    const float *t = &tile[r][c8];
-    const uint4 w = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]), pack_bf16(t[4], t[5]), pack_bf16(t[6], t[7]));
+    float mn = -INFINITY, f[SG], sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < SG; ++g) mn = fmaxf(mn, ml[g][0][r]);
+#pragma unroll
+    for (int g = 0; g < SG; ++g) {
+        f[g] = ml[g][0][r] == -INFINITY ? 0.f : ex2(ml[g][0][r] - mn);
+        sum = fmaf(ml[g][1][r], f[g], sum);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float x = 0.f;
+#pragma unroll
+        for (int g = 0; g < SG; ++g) x = fmaf(tile[g][r][c8 + i], f[g], x);
+        o[i] = x * inv;
+    }
+    const uint4 w = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
     const size_t at = (size_t)(tok + (rr >> p.g_shift)) * p.Hq + head + (rr & ((1 << p.g_shift) - 1));
     *reinterpret_cast<uint4 *>(p.out + at * D + blockIdx.z * 32 + c8) = w;
 }
@@ -1405,8 +1430,10 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
     const unsigned ctas = (unsigned)(p.part || items > sms ? sms : items);
     e = launch_pdl(multi_attn_kernel<D>, dim3(ctas), dim3(kThreads), L::kBytes, st, mQ, mK, mV, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch_pdl(multi_join_kernel<D>, dim3(items < sms ? (unsigned)items : ctas, kItemRows / 32, D / 32), dim3(128), 0,
-                      st, p);
+    const dim3 grid(items < sms ? (unsigned)items : ctas, kItemRows / 32, D / 32);
+    // about sms / items states an item: above 6, 4 groups of warps read them
+    if (sms > 6 * items) return launch_pdl(multi_join_kernel<D, 4>, grid, dim3(512), 0, st, p);
+    return launch_pdl(multi_join_kernel<D, 1>, grid, dim3(128), 0, st, p);
 }
 
 }  // namespace
