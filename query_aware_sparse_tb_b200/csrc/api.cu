@@ -410,6 +410,8 @@ static tb_status check_multi_shape(const tb_dims *dims, int32_t n_tokens, int32_
         return fail(TB_ERR_UNSUPPORTED, "%s: more than 2^31 - 256 cache rows", fn);
     if ((long long)n_tokens * dims->n_q_heads > 0x7fffffffLL)
         return fail(TB_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query rows", fn);
+    if (((long long)n_tokens + dims->batch) * dims->n_kv_heads > (1LL << 30))
+        return fail(TB_ERR_UNSUPPORTED, "%s: tokens and sequences times KV heads above 2^30", fn);
     return TB_OK;
 }
 

@@ -86,7 +86,7 @@ struct Lay {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kOperand;
     static constexpr int kBar = kRing + kStages * kOperand;
-    static constexpr int kNumBars = 2 * kStages + 37;
+    static constexpr int kNumBars = 2 * kStages + 38;
     static constexpr int kMisc = kBar + kNumBars * 8;       // TMEM base, abort flag
     static constexpr int kSeg = (kMisc + 8 + 15) / 16 * 16; // two segment descriptions
     static constexpr int kBad = kSeg + 2 * 64;              // two lists of V rows taken out of the product
@@ -353,24 +353,37 @@ __device__ __forceinline__ T warp_prefix(const Params &p, T v, int lane) {
     return v;
 }
 
-// All lanes of a warp: sequence and number within it of item `tau`, counted
-// over the sequences in packing order.
-__device__ __forceinline__ bool find_item(const Params &p, int tau, int lane, Seq &q, int &item) {
-    int before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const Seq mine = load_seq(p, b0 + lane);
-        const int items = items_of(p, mine.kept), incl = warp_prefix(p, items, lane);
-        const uint32_t hit = __ballot_sync(kFullMask, tau < before + incl);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            q = shfl_seq(mine, l);
-            item = tau - before - __shfl_sync(kFullMask, incl - items, l);
-            return true;
+// Sequence and number within it of item `tau`, counted over the sequences in
+// packing order, 32 sequences at a time by all lanes of a warp.  A CTA's items
+// come from the last to the first, so the search goes on from where it was.
+struct ItemSearch {
+    int b0 = 0, before = 0;  // the 32 sequences looked at last, items before them
+    __device__ __forceinline__ bool find(const Params &p, int tau, int lane, Seq &q, int &item) {
+        for (bool back = false; b0 < p.batch;) {
+            const Seq mine = load_seq(p, b0 + lane);
+            const int items = items_of(p, mine.kept), incl = warp_prefix(p, items, lane);
+            const int all = __shfl_sync(kFullMask, incl, 31);
+            if (back) before -= all;
+            if (tau < before) {
+                b0 -= 32;
+                back = true;
+                continue;
+            }
+            const uint32_t hit = __ballot_sync(kFullMask, tau < before + incl);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                q = shfl_seq(mine, l);
+                item = tau - before - (l > 0 ? __shfl_sync(kFullMask, incl, l > 0 ? l - 1 : 0) : 0);
+                return true;
+            }
+            if (b0 + 32 >= p.batch) return false;  // behind the last item
+            before += all;
+            b0 += 32;
+            back = false;
         }
-        before += __shfl_sync(kFullMask, incl, 31);
+        return false;
     }
-    return false;
-}
+};
 
 // Shares: the tiles of all items in one line (sequences in packing order, its
 // items in order, KV heads inside an item), each as long as it takes.  A tile
@@ -430,6 +443,13 @@ struct Shares {
     }
 };
 
+// Rows of an item's slots behind its last token hold queries of other
+// sequences or of nobody.  Where they are a quarter or more, warp 11 clears
+// them before the products use them: products with zeros draw less power, and
+// power is what bounds the clock (16 ragged trees: 415 -> 391 us; the look at
+// the queries costs about 0.4 us an item).
+__device__ __forceinline__ bool many_dead(int live, int rows) { return 4 * (rows - live) >= rows; }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -457,6 +477,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     auto o_done = [&](int s) { return bar(kB + 17 + s); };
     auto s_read = [&](int s) { return bar(kB + 19 + s); };
     auto v_loading = [&](int m) { return bar(kB + 21 + (m & 7)); };
+    const uint32_t q_raw = bar(kB + 37);
     auto v_clean = [&](int m) { return bar(kB + 29 + (m & 7)); };
     auto seg = [&](int i) { return reinterpret_cast<volatile int *>(sm + L::kSeg + i * 64); };
 
@@ -467,6 +488,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             mbar_init(empty(s), 1);
         }
         mbar_init(q_full, 1);
+        mbar_init(q_raw, 1);
         mbar_init(q_empty, 1);
         mbar_init(drain, 1);
         mbar_init(loaded, 1);
@@ -558,6 +580,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (p.part == nullptr) {
                 // from the last item to the first: a sequence's last tokens have the most tiles
                 bool first_item = true;
+                ItemSearch search;
                 while (ok) {
                     // the next item is taken when the current one's last tiles
                     // are on their way: early enough to overlap, and no CTA
@@ -573,7 +596,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (next >= p.item_bound * p.Hkv) break;
                     Seq q;
                     int item;
-                    if (!find_item(p, p.item_bound - 1 - next / p.Hkv, lane, q, item)) continue;
+                    if (!search.find(p, p.item_bound - 1 - next / p.Hkv, lane, q, item)) continue;
                     const int g = next % p.Hkv, tiles = item_tiles(p, q, item);
                     if (item == 0 && g == 0) report(q);
                     if (tiles > 0)
@@ -708,11 +731,12 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 if (!ok) break;
                 if (lane == 0) {
                     const int qn = pair ? 2 : 1, tok = f[kTok], head = f[kHead];
-                    mbar_arrive_expect_tx(q_full, (uint32_t)(qn * L::kOperand));
+                    const uint32_t qb = many_dead(f[kNTok] << p.g_shift, qn * kSlotRows) ? q_raw : q_full;
+                    mbar_arrive_expect_tx(qb, (uint32_t)(qn * L::kOperand));
                     for (int s = 0; s < qn; ++s)
 #pragma unroll
                         for (int a = 0; a < L::kAtoms; ++a)
-                            tma_load_3d(sb + s * L::kOperand + a * 16384, &tmQ, q_full, a * 64, head, tok + s * tps);
+                            tma_load_3d(sb + s * L::kOperand + a * 16384, &tmQ, qb, a * 64, head, tok + s * tps);
                 }
                 ++queries;
                 auto load = [&](bool is_k, int tile) {
@@ -762,7 +786,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // past the length, which may hold anything, are cleared; so are
             // rows with a value that is not finite, and listed: the epilogue
             // adds those to the tokens that see them.
-            int masked = 0, ring = 0;
+            int masked = 0, ring = 0, raws = 0;
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = wait_warp(seg_full(k & 1), (k >> 1) & 1, abort_flag, p.flags);
@@ -774,6 +798,22 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 volatile int *bad = reinterpret_cast<volatile int *>(sm + L::kBad + (k & 1) * kBadBytes);
                 if (lane == 0) bad[0] = 0;
                 __syncwarp();
+                const int live = f[kNTok] << p.g_shift, rows = f[kPair] ? kItemRows : kSlotRows;
+                if (many_dead(live, rows)) {
+                    ok = wait_warp(q_raw, raws & 1, abort_flag, p.flags);
+                    if (!ok) break;
+                    ++raws;
+                    for (int r = live; r < rows; r += 4)
+                        for (int a = 0; a < L::kAtoms; ++a) {
+                            const int rr = r + (lane >> 3);
+                            if (rr < rows)
+                                *reinterpret_cast<uint4 *>(sm + (rr >> 7) * L::kOperand + a * 16384 + (rr & 127) * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full);
+                }
                 int n_bad = 0;
                 for (int t = max(0, mask_lo / kTile); t < nt && ok; ++t) {
                     if ((t + 1) * kTile <= mask_lo) continue;

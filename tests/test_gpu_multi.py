@@ -738,3 +738,96 @@ def test_calls_of_no_tokens_do_nothing():
                         False, Q, K, V, ws)
     torch.cuda.synchronize()
     assert tb.workspace_check(ws) == 0 and torch.equal(K, want) and torch.equal(V, want)
+
+
+# ------------------------------------------------------------------ many sequences, long caches
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tree", [False, True])
+def test_more_sequences_than_a_warp_looks_at_once(tree, d):
+    r = np.random.RandomState(40 + d)
+    n = [int(x) for x in r.choice([0, 1, 2, 5, 40, 70], 100)]
+    T = [k + int(x) for k, x in zip(n, r.choice([0, 3, 200, 700], 100))]
+    if tree:
+        masks = [random_tree(k, r) for k in n]
+        Q, K, V, out, scale = run_tree(n, T, masks, 8, 2, d, seed=1)
+        see = tree_see(masks, n, T)
+    else:
+        Q, K, V, out, scale = run_prompt(n, T, 8, 2, d, seed=1)
+        see = causal(n, T)
+    ref, tol = reference(Q, K, V, n, T, scale, see)
+    check(out[:sum(n)], ref[:sum(n)], tol[:sum(n)])
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^31 elements: the last (sequence, KV head) lies
+    past 4 GB of each of K and V, for the write, both attentions and the move."""
+    hq, hkv, d, cap = 4, 4, 128, (1 << 22)
+    assert hkv * cap * d >= 1 << 31
+    T, n = cap - 5, 6
+    g = torch.Generator(device=DEV).manual_seed(50)
+    kv = torch.zeros(1, 2, 1, hkv, cap, d, dtype=torch.bfloat16, device=DEV)
+    K, V = kv[0, 0], kv[0, 1]
+    lo = T - 3000                              # everything before has the same small key and zero value
+    K[..., :lo, :] = 0.125
+    K[:, :, lo:T] = torch.randn(1, hkv, 3000, d, generator=g, device=DEV).to(torch.bfloat16)
+    V[:, :, lo:T] = torch.randn(1, hkv, 3000, d, generator=g, device=DEV).to(torch.bfloat16)
+    dm = tb.dims(1, hq, hkv, d, 16, cap)
+    qkv = torch.randn(n, (hq + 2 * hkv) * d, generator=g, device=DEV).to(torch.bfloat16)
+    Q = torch.zeros(n, hq, d, dtype=torch.bfloat16, device=DEV)
+    qb, ctx, ws = i32([0, n]), i32([T]), tb.workspace(256)
+    tb.norm_rope_append(dm, qkv, qb, ctx, None, None, None, 0.0, None, False, Q, K, V, ws)
+    x = qkv.view(n, 3 * hkv, d)
+    assert torch.equal(K[0, :, T - n:T], x[:, hkv:2 * hkv].transpose(0, 1))
+    assert torch.equal(V[0, :, T - n:T], x[:, 2 * hkv:].transpose(0, 1)) and torch.equal(Q, x[:, :hkv])
+    scale = 0.05
+    mask = pack_rows(np.tril(np.ones((n, n), dtype=bool)), 1)
+    outs = []
+    for tree in (False, True):
+        out = torch.zeros_like(Q)
+        size = tb.tree_attn_workspace_bytes if tree else tb.prompt_attn_workspace_bytes
+        wsa = tb.workspace(size(dm, n, n))
+        if tree:
+            tb.tree_attn(dm, Q, K, V, qb, n, ctx, mask, scale, out, wsa)
+        else:
+            tb.prompt_attn(dm, Q, K, V, qb, n, ctx, scale, out, wsa)
+        assert tb.workspace_check(wsa) == 0
+        outs.append(out)
+    assert torch.equal(*outs)
+    # the rows before `lo` share one logit: lo times its weight in the denominator
+    for i in range(n):
+        end = T - n + i + 1
+        for h in range(hkv):
+            q = Q[i, h].to(F64)
+            k, v = K[0, h, lo:end].to(F64), V[0, h, lo:end].to(F64)
+            l = torch.cat([(q.sum() * 0.125)[None], k @ q]) * scale
+            p = torch.exp(l - l.max())
+            p[0] *= lo
+            ref, A = (p[1:] @ v) / p.sum(), (p[1:] @ v.abs()) / p.sum()
+            # fp32 sums of 2^22 terms, 128 at a time: the adds of a row's tiles, 2^15 e, and what `check` counts
+            tol = U * ref.abs() + A * (U + 2 * (2.0 ** -13 + 256 * E * 10) + 2 * E * 2 ** 15)
+            check(outs[0][i, h], ref, tol, f"token {i} head {h}")
+    before = kv[0, :, 0, :, T - n:T].clone()
+    new_len = torch.zeros(1, dtype=torch.int32, device=DEV)
+    caches = torch.tensor([K.data_ptr(), V.data_ptr()], dtype=torch.int64, device=DEV)
+    tb.tree_accept(dm, 1, caches, qb, ctx, i32([[1, 2, 5]]), i32([3]), new_len, ws)
+    assert tb.workspace_check(ws) == 0 and new_len.item() == T - n + 3
+    assert torch.equal(kv[0, :, 0, :, T - n:T - n + 3], before[:, :, [1, 2, 5]])
+    assert torch.equal(kv[0, :, 0, :, T - n + 3:T], before[:, :, 3:])
+
+
+def test_two_streams_at_once_with_workspaces_of_their_own():
+    cases = [([64, 9], [3000, 40], 128), ([200], [200], 64), ([5, 5, 5], [900, 2000, 5], 128)]
+    runs, streams = [], [torch.cuda.Stream() for _ in cases]
+    for k, (n, T, d) in enumerate(cases):
+        Q, K, V, out, scale = run_prompt(n, T, 8, 2, d, seed=60 + k, extra=0)
+        dm = tb.dims(len(n), 8, 2, d, 16, K.shape[2])
+        runs.append((dm, Q, K, V, i32(starts(n)), max(n), i32(T), scale, out,
+                     tb.workspace(tb.prompt_attn_workspace_bytes(dm, sum(n), max(n))), torch.zeros_like(out)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (dm, Q, K, V, qb, mx, ct, scale, out, ws, got) in zip(streams, runs):
+            tb.prompt_attn(dm, Q, K, V, qb, mx, ct, scale, got, ws, stream=s)
+    torch.cuda.synchronize()
+    for dm, Q, K, V, qb, mx, ct, scale, out, ws, got in runs:
+        assert torch.equal(got, out) and tb.workspace_check(ws) == 0
