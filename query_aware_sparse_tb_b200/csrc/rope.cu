@@ -58,34 +58,88 @@ __device__ __forceinline__ int find_seq(const int32_t *q_begin, int batch, int t
     return lo - 1;
 }
 
-__device__ __forceinline__ void unpack4(uint2 u, float *f) {
-    f[0] = bf16_lo(u.x);
-    f[1] = bf16_hi(u.x);
-    f[2] = bf16_lo(u.y);
-    f[3] = bf16_hi(u.y);
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 pack2(float lo, float hi) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-__device__ __forceinline__ uint2 pack4(const float *f) {
-    uint2 u;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(f[1]), "f"(f[0]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(f[3]), "f"(f[2]));
-    return u;
+__device__ __forceinline__ void unpack2(u64 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 sub2(u64 a, u64 b) {
+    u64 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
-template <int D>
+// A lane's 8 values of a head row as 4 pairs (x_j, y_j) of the rotation, held
+// as x_0 x_1 | x_2 x_3 and y_0 y_1 | y_2 y_3: half style pairs value k of the
+// first group with value k of the second, interleaved pairs neighbours.
+struct Pairs {
+    u64 x[2], y[2];
+};
+template <bool INTER>
+__device__ __forceinline__ Pairs unpack_pairs(uint2 a, uint2 b) {
+    if constexpr (INTER)
+        return {{pack2(bf16_lo(a.x), bf16_lo(a.y)), pack2(bf16_lo(b.x), bf16_lo(b.y))},
+                {pack2(bf16_hi(a.x), bf16_hi(a.y)), pack2(bf16_hi(b.x), bf16_hi(b.y))}};
+    else
+        return {{pack2(bf16_lo(a.x), bf16_hi(a.x)), pack2(bf16_lo(a.y), bf16_hi(a.y))},
+                {pack2(bf16_lo(b.x), bf16_hi(b.x)), pack2(bf16_lo(b.y), bf16_hi(b.y))}};
+}
+template <bool INTER>
+__device__ __forceinline__ void pack_pairs(const Pairs &p, uint2 &a, uint2 &b) {
+    float x[4], y[4];
+    unpack2(p.x[0], x[0], x[1]);
+    unpack2(p.x[1], x[2], x[3]);
+    unpack2(p.y[0], y[0], y[1]);
+    unpack2(p.y[1], y[2], y[3]);
+    if constexpr (INTER) {
+        a = make_uint2(pack_bf16(x[0], y[0]), pack_bf16(x[1], y[1]));
+        b = make_uint2(pack_bf16(x[2], y[2]), pack_bf16(x[3], y[3]));
+    } else {
+        a = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        b = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+    }
+}
+
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads)
 norm_rope_append_kernel(const RopeParams p) {
     constexpr int LPH = D / 8;    // lanes per head row
     constexpr int HPI = 32 / LPH; // head rows per warp instruction
     constexpr int kUnroll = 4;
     const int lane = threadIdx.x & 31;
-    const int warps_per_token = (p.Hq + 2 * p.Hkv + p.heads_per_warp - 1) / p.heads_per_warp;
+    const int heads = p.Hq + 2 * p.Hkv;
+    const int warps_per_token = (heads + p.heads_per_warp - 1) / p.heads_per_warp;
     griddep_wait();
     griddep_launch_dependents();
-    const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int tok = (int)(w / warps_per_token);
+    const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (the host keeps it below 2^31)
+    const int tok = w / warps_per_token;
     if (tok >= p.n_tokens) return;
-    const int h0 = (int)(w % warps_per_token) * p.heads_per_warp;
-    const int h1 = min(h0 + p.heads_per_warp, p.Hq + 2 * p.Hkv);
+    const int h0 = (w - tok * warps_per_token) * p.heads_per_warp;
+    const int h1 = min(h0 + p.heads_per_warp, heads);
     const int b = find_seq(p.q_begin, p.batch, tok, lane);
     if (b < 0) return;
     const SeqSpan sp = seq_span(p.q_begin, b, p.n_tokens);
@@ -95,20 +149,13 @@ norm_rope_append_kernel(const RopeParams p) {
     if (!cached && h0 == 0 && lane == 0) raise_flag(p.flags, TB_FLAG_CTX_RANGE);
 
     // this lane's two groups of 4 values: half style pairs group r with group
-    // r + R (R = rot / 8); interleaved pairs lie within a group
-    const int l = lane % LPH, R = p.rot / 8;
-    int ga, gb;
-    bool ra, rb;  // does the group turn?
-    if (p.interleaved) {
-        ga = 2 * l;
-        gb = 2 * l + 1;
-        ra = ga * 4 < p.rot;
-        rb = gb * 4 < p.rot;
-    } else {
-        ra = rb = l < R;
-        ga = l < R ? l : l + R;
-        gb = l < R ? l + R : l + LPH;
-    }
+    // r + R (R = rot / 8) and leaves the groups from 2 R on alone
+    const int l = lane % LPH, hl = lane / LPH, R = p.rot / 8;
+    const int ga = INTER ? 2 * l : l < R ? l : l + R;
+    const int gb = INTER ? 2 * l + 1 : l < R ? l + R : l + LPH;
+    // which of the lane's pairs turn (rot is a multiple of 8, so in half style
+    // all or none, in interleaved style those of a group alike)
+    const bool ra = INTER ? ga * 4 < p.rot : l < R, rb = INTER ? gb * 4 < p.rot : l < R;
     // cosines and sines of the lane's 4 pairs: the HPI lanes that hold the same
     // values of different heads work out 4 / HPI of them each and trade
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
@@ -117,7 +164,7 @@ norm_rope_append_kernel(const RopeParams p) {
         float c[4 / HPI], s[4 / HPI];
 #pragma unroll
         for (int i = 0; i < 4 / HPI; ++i) {
-            const int j = 4 * l + i * HPI + lane / LPH;  // the pair's frequency
+            const int j = 4 * l + i * HPI + hl;  // the pair's frequency
             double t = 0.0;
             if (j < p.rot / 2) t = P * p.inv_freq[j] * 0.31830988618379067154;  // half turns
             t -= 2.0 * rint(0.5 * t);
@@ -130,88 +177,80 @@ norm_rope_append_kernel(const RopeParams p) {
         }
     }
 
-    const uint16_t *src = p.qkv + (size_t)tok * p.row_stride;
-    const size_t kv0 = ((size_t)b * p.Hkv * p.cap + (cached ? row : 0)) * D;
-    for (int hb = h0; hb < h1; hb += HPI * kUnroll) {
-        uint2 ua[kUnroll], ub[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = hb + u * HPI + lane / LPH;
-            ua[u] = ub[u] = make_uint2(0u, 0u);
-            if (h < h1) {
-                const uint2 *r = reinterpret_cast<const uint2 *>(src + (size_t)h * D);
-                ua[u] = r[ga];
-                ub[u] = r[gb];
-            }
+    const u64 c2[2] = {pack2(cs[0], cs[1]), pack2(cs[2], cs[3])}, s2[2] = {pack2(sn[0], sn[1]), pack2(sn[2], sn[3])};
+
+    // the heads in three runs: queries, keys, values; in each kUnroll rows a
+    // lane are requested before the first is worked on
+    const uint2 *src = reinterpret_cast<const uint2 *>(p.qkv + (size_t)tok * p.row_stride);
+    auto run = [&](int begin, int end, uint16_t *out, uint32_t step, auto turn_c, const uint16_t *weight) {
+        constexpr bool kTurn = decltype(turn_c)::value;
+        const int hb = max(begin, h0), he = min(end, h1);
+        if (hb >= he) return;
+        Pairs wt{};
+        if (kTurn && weight) {
+            const uint2 *r = reinterpret_cast<const uint2 *>(weight);
+            wt = unpack_pairs<INTER>(__ldg(r + ga), __ldg(r + gb));
         }
+        uint2 *dst = reinterpret_cast<uint2 *>(out);
+        for (int h = hb + hl; h - hl < he; h += HPI * kUnroll) {
+            uint2 ua[kUnroll], ub[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = hb + u * HPI + lane / LPH;
-            const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-            uint2 oa = ua[u], ob = ub[u];
-            if (hb + u * HPI < p.Hq + p.Hkv) {  // (uniform: some head of the warp is q or k)
-                float a[4], c[4];
-                unpack4(oa, a);
-                unpack4(ob, c);
-                if (p.qw || p.kw) {
-                    float ss = 0.f;
+            for (int u = 0; u < kUnroll; ++u) {
+                ua[u] = ub[u] = make_uint2(0u, 0u);
+                if (h + u * HPI < he) {
+                    const uint2 *r = src + (uint32_t)((h + u * HPI) * (D / 4));
+                    ua[u] = r[ga];
+                    ub[u] = r[gb];
+                }
+            }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) ss = fmaf(a[k], a[k], fmaf(c[k], c[k], ss));
+            for (int u = 0; u < kUnroll; ++u) {
+                if (h - hl + u * HPI >= he) break;  // (the same for all lanes)
+                if constexpr (kTurn) {
+                    Pairs v = unpack_pairs<INTER>(ua[u], ub[u]);
+                    if (weight) {
+                        u64 q2 = mul2(v.x[0], v.x[0]);
+                        q2 = fma2(v.y[0], v.y[0], q2);
+                        q2 = fma2(v.x[1], v.x[1], q2);
+                        q2 = fma2(v.y[1], v.y[1], q2);
+                        float s0, s1;
+                        unpack2(q2, s0, s1);
+                        float ss = s0 + s1;
 #pragma unroll
-                    for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-                    const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-                    const uint2 *wr = reinterpret_cast<const uint2 *>(is_q ? p.qw : p.kw);
-                    if (wr) {
-                        float wa[4], wb[4];
-                        unpack4(__ldg(wr + ga), wa);
-                        unpack4(__ldg(wr + gb), wb);
+                        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+                        const float inv = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+                        const u64 inv2 = pack2(inv, inv);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            a[k] *= inv * wa[k];
-                            c[k] *= inv * wb[k];
+                        for (int i = 0; i < 2; ++i) {
+                            v.x[i] = mul2(mul2(v.x[i], inv2), wt.x[i]);
+                            v.y[i] = mul2(mul2(v.y[i], inv2), wt.y[i]);
                         }
                     }
-                }
-                if (p.interleaved) {
-                    if (ra) {
-                        const float x0 = a[0], x1 = a[1], x2 = a[2], x3 = a[3];
-                        a[0] = x0 * cs[0] - x1 * sn[0];
-                        a[1] = x1 * cs[0] + x0 * sn[0];
-                        a[2] = x2 * cs[1] - x3 * sn[1];
-                        a[3] = x3 * cs[1] + x2 * sn[1];
-                    }
-                    if (rb) {
-                        const float x0 = c[0], x1 = c[1], x2 = c[2], x3 = c[3];
-                        c[0] = x0 * cs[2] - x1 * sn[2];
-                        c[1] = x1 * cs[2] + x0 * sn[2];
-                        c[2] = x2 * cs[3] - x3 * sn[3];
-                        c[3] = x3 * cs[3] + x2 * sn[3];
-                    }
-                } else if (ra) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float x = a[k], y = c[k];
-                        a[k] = x * cs[k] - y * sn[k];
-                        c[k] = y * cs[k] + x * sn[k];
+                    for (int i = 0; i < 2; ++i) {
+                        // (pairs that do not turn keep apart: a NaN in one is no business of the other's)
+                        if (INTER ? (i ? rb : ra) : ra) {
+                            const u64 x = v.x[i], y = v.y[i];
+                            v.x[i] = sub2(mul2(x, c2[i]), mul2(y, s2[i]));
+                            v.y[i] = fma2(x, s2[i], mul2(y, c2[i]));
+                        }
                     }
+                    pack_pairs<INTER>(v, ua[u], ub[u]);
                 }
-                if (is_q || is_k) {
-                    oa = pack4(a);
-                    ob = pack4(c);
+                if (h + u * HPI < he) {
+                    uint2 *r = dst + (size_t)(uint32_t)(h + u * HPI - begin) * step;
+                    r[ga] = ua[u];
+                    r[gb] = ub[u];
                 }
             }
-            if (h >= h1 || (!is_q && !cached)) continue;
-            uint16_t *dst;
-            if (is_q)
-                dst = p.Q + ((size_t)tok * p.Hq + h) * D;
-            else if (is_k)
-                dst = p.K + kv0 + (size_t)(h - p.Hq) * p.cap * D;
-            else
-                dst = p.V + kv0 + (size_t)(h - p.Hq - p.Hkv) * p.cap * D;
-            reinterpret_cast<uint2 *>(dst)[ga] = oa;
-            reinterpret_cast<uint2 *>(dst)[gb] = ob;
         }
-    }
+    };
+    run(0, p.Hq, p.Q + (size_t)tok * p.Hq * D, D / 4, Flag<true>{}, p.qw);
+    if (!cached) return;
+    const size_t kv0 = ((size_t)b * p.Hkv * p.cap + row) * D;
+    const uint32_t kv_step = (uint32_t)p.cap * (D / 4);  // one KV head, in groups (cap <= 2^22)
+    run(p.Hq, p.Hq + p.Hkv, p.K + kv0, kv_step, Flag<true>{}, p.kw);
+    run(p.Hq + p.Hkv, heads, p.V + kv0, kv_step, Flag<false>{}, nullptr);
 }
 
 }  // namespace
@@ -248,8 +287,9 @@ cudaError_t launch_norm_rope_append(const tb_dims &d, const uint16_t *qkv, int64
     p.heads_per_warp = n_tokens >= num_sms() * 16 ? heads : round;
     const long long warps = (long long)n_tokens * ((heads + p.heads_per_warp - 1) / p.heads_per_warp);
     const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
-    if (d.head_dim == 128) return launch_pdl(norm_rope_append_kernel<128>, grid, dim3(kThreads), 0, st, p);
-    return launch_pdl(norm_rope_append_kernel<64>, grid, dim3(kThreads), 0, st, p);
+    auto *kernel = d.head_dim == 128 ? (p.interleaved ? norm_rope_append_kernel<128, true> : norm_rope_append_kernel<128, false>)
+                                     : (p.interleaved ? norm_rope_append_kernel<64, true> : norm_rope_append_kernel<64, false>);
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, p);
 }
 
 }  // namespace tb
