@@ -517,10 +517,13 @@ tb_status tb_sparse_decode_attn_noalloc(const tb_dims *dims, const tb_bf16 *Q, c
  *   q_weight, k_weight  [d] bf16, either may be NULL: that norm is left out
  *   inv_freq  [rot_dim / 2] double (device, 8-byte aligned), radians per
  *             position; rot_dim a multiple of 8 in [0, d] (0: no rotation)
- *   Q         [n_tokens][Hq][d] bf16 out; must not overlap qkv
+ *   Q         [n_tokens][Hq][d] bf16 out
  *   K, V      the caches: row T - n + i of every KV head written
- * A token whose cache row lies outside [0, ctx_cap) gets its Q row only, and
- * TB_FLAG_CTX_RANGE is raised in ws (>= 256 bytes). */
+ * qkv, Q, K and V must not overlap.  A token whose cache row lies outside [0,
+ * ctx_cap) gets its Q row only, and TB_FLAG_CTX_RANGE is raised in ws (>= 256
+ * bytes).  A row whose squares overflow fp32 (values past 10^19) comes out 0.
+ * An attention call that follows in TB_ATTN_PREFETCH_KV mode may read only
+ * what this call does not write: it must not follow a call with n > 1. */
 #define TB_ROPE_HALF 0
 #define TB_ROPE_INTERLEAVED 1
 tb_status tb_norm_rope_append(const tb_dims *dims, const tb_bf16 *qkv, int64_t row_stride, const int32_t *q_begin,
@@ -581,7 +584,8 @@ tb_status tb_tree_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, 
  * or leaves [0, n) moves nothing, keeps new_len[b] = T and raises
  * TB_FLAG_BAD_PATH in ws (>= 256 bytes); so does n outside [0, T] or T above
  * ctx_cap.  Projected keys (K') are not touched: project only rows below the
- * accepted length. */
+ * accepted length.  The attention call that follows must not be in
+ * TB_ATTN_PREFETCH_KV mode (rows below its T - 1 are written here). */
 tb_status tb_tree_accept(const tb_dims *dims, int32_t n_layers, const uint64_t *caches, const int32_t *q_begin,
                          const int32_t *ctx_len, const int32_t *path, int32_t path_cap, const int32_t *path_len,
                          int32_t *new_len, void *ws, size_t ws_bytes, void *stream);

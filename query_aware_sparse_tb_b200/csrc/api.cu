@@ -390,8 +390,12 @@ tb_status tb_norm_rope_append(const tb_dims *dims, const tb_bf16 *qkv, int64_t r
         return fail(TB_ERR_INVALID_ARG, "%s: unknown style %d", __func__, style);
     if ((long long)n_tokens * ((dims->n_q_heads + 2LL * dims->n_kv_heads + 7) / 8) > 0x7fffffffLL)
         return fail(TB_ERR_UNSUPPORTED, "%s: n_tokens %d times the heads is too large for one call", __func__, n_tokens);
-    if (overlap(Q, (size_t)n_tokens * dims->n_q_heads * dims->head_dim * 2, qkv, (size_t)n_tokens * row_stride * 2))
-        return fail(TB_ERR_INVALID_ARG, "%s: Q overlaps qkv", __func__);
+    const size_t in = ((size_t)(n_tokens - 1) * row_stride + width) * 2;
+    const size_t qb = (size_t)n_tokens * dims->n_q_heads * dims->head_dim * 2;
+    const size_t kb = (size_t)dims->batch * dims->n_kv_heads * dims->ctx_cap * dims->head_dim * 2;
+    if (overlap(Q, qb, qkv, in) || overlap(K, kb, qkv, in) || overlap(V, kb, qkv, in) || overlap(Q, qb, K, kb) ||
+        overlap(Q, qb, V, kb) || overlap(K, kb, V, kb))
+        return fail(TB_ERR_INVALID_ARG, "%s: Q, K, V and qkv overlap", __func__);
     if ((s = check_ws(ws, ws_bytes, kWsHeaderBytes, __func__)) != TB_OK) return s;
     return cuda_status(launch_norm_rope_append(*dims, qkv, row_stride, q_begin, n_tokens, ctx_len, pos, q_weight,
                                                k_weight, eps, inv_freq, rot_dim, style, Q, K, V, ws,

@@ -25,9 +25,10 @@
 // Warps: 0-3 softmax of slot 0, 4-7 softmax of slot 1, 8 issues the products,
 // 9 loads (TMA), 10 schedules, 11 looks over the V tiles that are masked for
 // some rows.  These four need few registers; the softmax warps take the rest
-// (a softmax thread holds a whole row of a tile, 128 logits).  Tensor memory: S0 | S1 | O0 | O1, 128 columns each; the weights
-// P (bf16) overwrite the first half of their S columns and are read from there
-// as the A operand of the second product.
+// (a softmax thread holds a whole row of a tile, 128 logits).  Tensor memory:
+// S0 | S1 | O0 | O1, 128 columns each; the weights P (bf16) overwrite the first
+// half of their S columns (at 64 head dims they have columns of their own) and
+// are read from there as the A operand of the second product.
 //
 // The grid is one CTA per SM, each working through a list of segments (an item
 // or a part of its K/V tiles) that warp 10 describes to the other warps one
@@ -38,6 +39,19 @@
 //     into equal shares.  A CTA's share may begin and end inside an item; such
 //     parts leave their rows' unnormalised state in the workspace and a second
 //     kernel joins them.
+//
+// What bounds it, on a B200 (32 query heads, 8 KV heads, 128 head dims):
+//   - long prompts: the tensor cores and the power they draw.  A tile of 256
+//     rows x 128 keys is 2,048 cycles of products and takes about 3,100, the
+//     rest being the latency of the chain S, softmax, PV within a slot; 32K
+//     tokens run 6.7 ms from a cold GPU (1,310 TFLOP/s) and 7.5 ms once the
+//     power cap holds the clock near 1.55 GHz (1,165 TFLOP/s; a plain bf16
+//     matrix product does 1,400 there).
+//   - 64 head dims: the softmax (the products are half as long, the
+//     exponentials as many): 735 TFLOP/s at 8K tokens.
+//   - trees and decode steps over long contexts: HBM.  26 drafted tokens over
+//     64K rows stream 269 MB in 37 of 56 us; the rest is the start (5 us), the
+//     states (3 us) and their join (5 us).
 #include <cuda.h>
 #include <math.h>
 
@@ -54,7 +68,7 @@ constexpr int kTile = 128;                  // K/V rows per tile
 constexpr int kThreads = 384;
 // Registers a thread: 168 at launch (384 threads fill the file); the third
 // warpgroup gives most of its share to the two softmax warpgroups
-// (2 * 128 * 224 + 128 * 56 = 384 * 168).
+// (2 * 128 * 216 + 128 * 72 = 384 * 168).
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;
@@ -65,7 +79,10 @@ constexpr uint32_t kTmemCols = 512;
 // exponents; the sums (weights x 2^22 rows x |v|) stay finite to |v| of 2^72.
 // At 8 an 8K prompt with 1% of its keys scaled by 4 took 540 us, at 32 505.
 constexpr float kLazy = 32.0f;
-constexpr int kPolyOf8 = 2;                 // of 8 pairs of weights, those worked out on the FMA pipe
+// Of 8 pairs of weights, those worked out on the FMA pipe: the exponential
+// unit's 16 a cycle would take as long as the products.  0 to 4 of 8 measured
+// within 3% at 128 head dims (the power cap evens them out); at 64, 2 was best.
+constexpr int kPolyOf8 = 2;
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 // Masked tiles of an item: its new tokens' rows (1024 at most for a tree, 256
@@ -279,6 +296,7 @@ struct Params {
     int batch, Hq, Hkv, cap, n_tokens, max_new, mask_words;
     int g_shift;            // G = 1 << g_shift heads per group
     int item_bound;         // items of a KV head, at most
+    int ctas;               // CTAs of multi_attn_kernel
     float c;                // scale * log2(e)
 };
 
@@ -1322,6 +1340,10 @@ multi_join_kernel(const Params p) {
     // CTAs from .. from + n - 1: state 2 c + 1 of the first, 2 c of the others
     const int from = e.x, n = e.y, tok = e.z, head = e.w;
     if (from < 0 || (int)blockIdx.y * 32 >= rows) return;
+    // (entries of a call whose waits ran out may be anything: stay in the arrays)
+    if (n < 1 || from + n > p.ctas || rows > kItemRows || tok < 0 || tok + (rows >> p.g_shift) > p.n_tokens ||
+        head < 0 || head + (1 << p.g_shift) > p.Hq)
+        return;
     constexpr size_t kRec = (size_t)(D + 2) * kItemRows;
     const int d0 = blockIdx.z * 32 + dg * 8;
     const float *base = p.part + blockIdx.y * 32 + lane;
@@ -1468,6 +1490,7 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
     if (e != cudaSuccess) return e;
     const long long items = (long long)p.item_bound * p.Hkv, sms = num_sms();
     const unsigned ctas = (unsigned)(p.part || items > sms ? sms : items);
+    p.ctas = (int)ctas;
     e = launch_pdl(multi_attn_kernel<D>, dim3(ctas), dim3(kThreads), L::kBytes, st, mQ, mK, mV, p);
     if (e != cudaSuccess || !p.part) return e;
     const dim3 grid(items < sms ? (unsigned)items : ctas, kItemRows / 32, D / 32);
