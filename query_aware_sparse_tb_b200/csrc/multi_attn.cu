@@ -79,10 +79,6 @@ constexpr uint32_t kTmemCols = 512;
 // exponents; the sums (weights x 2^22 rows x |v|) stay finite to |v| of 2^72.
 // At 8 an 8K prompt with 1% of its keys scaled by 4 took 540 us, at 32 505.
 constexpr float kLazy = 32.0f;
-// Of 8 pairs of weights, those worked out on the FMA pipe: the exponential
-// unit's 16 a cycle would take as long as the products.  0 to 4 of 8 measured
-// within 3% at 128 head dims (the power cap evens them out); at 64, 2 was best.
-constexpr int kPolyOf8 = 2;
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 // Masked tiles of an item: its new tokens' rows (1024 at most for a tree, 256
@@ -177,34 +173,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-// 2^x for a pair on the FMA pipe: x = n + f with n the nearest integer, 2^f by
-// a cubic with the smallest largest relative error on [-1/2, 1/2] (1.02e-4,
-// fitted for this kernel; 2^0 = 1 exactly; the weights' rounding to bf16 is up
-// to 40 times that), n added to the exponent.  x is
-// held at -127 or above, where the result is exactly 0.
-__device__ __forceinline__ void ex2_poly2(uint64_t x2, float &e0, float &e1) {
-    float a, b;
-    unpack2(x2, a, b);
-    const uint64_t x = pack2(fmaxf(a, -127.f), fmaxf(b, -127.f));
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
-    const uint64_t t = add2(x, pack2(kMagic, kMagic));
-    const uint64_t n = add2(t, pack2(-kMagic, -kMagic));
-    const uint64_t f = sub2(x, n);
-    uint64_t r = fma2(f, pack2(0.05500893294811249f, 0.05500893294811249f),
-                      pack2(0.24221095442771912f, 0.24221095442771912f));
-    r = fma2(r, f, pack2(0.6932829022407532f, 0.6932829022407532f));
-    r = fma2(r, f, pack2(1.f, 1.f));
-    float t0, t1, r0, r1;
-    unpack2(t, t0, t1);
-    unpack2(r, r0, r1);
-    e0 = __uint_as_float(__float_as_uint(r0) + (__float_as_uint(t0) << 23));
-    e1 = __uint_as_float(__float_as_uint(r1) + (__float_as_uint(t1) << 23));
 }
 // The largest of three; NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -1165,14 +1133,14 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int i = 0; i < 16; ++i) {
                         const uint64_t x2 =
                             fma2(pack2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
+                        // (a quarter of the exponentials by a polynomial on
+                        // the FMA pipe, beside the unit's 16 a cycle, made no
+                        // difference under the power cap: 510 against 512 us
+                        // for an 8K prompt)
                         float e0, e1;
-                        if ((i & 7) < kPolyOf8) {
-                            ex2_poly2(x2, e0, e1);
-                        } else {
-                            unpack2(x2, e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                        }
+                        unpack2(x2, e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
                         sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
                         // rounded to bf16 for the second product: 2^-9 relative
                         // per weight, below the rounding of the bf16 result
@@ -1463,14 +1431,16 @@ long long item_bound(const tb_dims &d, int32_t n_tokens, int32_t max_new) {
 // of the longest context the cache holds (the lengths are the device's): whole
 // items take the average load and, at the end, about half of the smallest item
 // that may come last; at least one whole item.  Shares are even but write and
-// join states, about 8 tiles' time.
+// join states, about 16 tiles' time
+// (992 items of 25 to 64 tiles: 371 us in shares, 358 by the counter; 16 items of
+// 514 tiles: 141 against 838).
 bool use_shares(const tb_dims &d, int32_t max_new, bool tree, long long items) {
     const double ctas = num_sms(), n = (double)items * d.n_kv_heads;
     const double longest = (d.ctx_cap + kTile - 1) / kTile;
     const double shortest = tree ? longest : fmax(1.0, (double)(d.ctx_cap - max_new) / kTile);
     const double average = 0.5 * (longest + shortest);
     const double whole = fmax(longest, n * average / ctas + 0.5 * shortest);
-    return n * average / ctas + 8.0 < whole;
+    return n * average / ctas + 16.0 < whole;
 }
 
 template <int D>

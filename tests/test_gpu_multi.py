@@ -10,8 +10,7 @@ relative error, e = 2^-24 an fp32 one's.
              sum p, N the row's number of terms and w the largest error of a
              weight's exponent: the fp32 dot product (d e sum|q k| scale), the
              product and difference in log2 units (4 e (|l| + 8)) and the
-             exponential (2^-13: a quarter of the weights come from a cubic
-             whose largest relative error is 1.02e-4); twice, for numerator and denominator.  The
+             exponential (2^-21); twice, for numerator and denominator.  The
              u in the brackets is the weights' rounding before the product
              with V.
   rotation   |y - ref| <= u |ref| + 24 e (|a| + |b|) for a pair (a, b): about
@@ -79,7 +78,7 @@ def reference(Q, K, V, n, T, scale, see):
                 den = torch.where(dead, 1.0, den)
                 o = (p @ v) / den
                 A = (p @ v.abs()) / den
-                w = d * E * mag.masked_fill(~ok, 0).amax(1) + 4 * E * (l.masked_fill(~ok, 0).abs().amax(1) * 1.45 + 8) + 2.0 ** -13
+                w = d * E * mag.masked_fill(~ok, 0).amax(1) + 4 * E * (l.masked_fill(~ok, 0).abs().amax(1) * 1.45 + 8) + 2.0 ** -21
                 N = ok.sum(1)
                 ref[s[b] + i0:s[b] + i1, h] = o
                 tol[s[b] + i0:s[b] + i1, h] = U * o.abs() + A * (U + 2 * w + 2 * E * N)[:, None]
@@ -805,7 +804,7 @@ def test_offsets_past_32_bits():
             p[0] *= lo
             ref, A = (p[1:] @ v) / p.sum(), (p[1:] @ v.abs()) / p.sum()
             # fp32 sums of 2^22 terms, 128 at a time: the adds of a row's tiles, 2^15 e, and what `check` counts
-            tol = U * ref.abs() + A * (U + 2 * (2.0 ** -13 + 256 * E * 10) + 2 * E * 2 ** 15)
+            tol = U * ref.abs() + A * (U + 2 * (2.0 ** -21 + 256 * E * 10) + 2 * E * 2 ** 15)
             check(outs[0][i, h], ref, tol, f"token {i} head {h}")
     before = kv[0, :, 0, :, T - n:T].clone()
     new_len = torch.zeros(1, dtype=torch.int32, device=DEV)
