@@ -260,7 +260,7 @@ struct Params {
     uint16_t *out;
     float *part;            // shares: two states per CTA; nullptr: the counter deals whole items out
     int32_t *joins;         // shares: what to join, 8 words an entry (first CTA or -1, CTAs, token, head, rows)
-    uint32_t *flags, *counter;  // counter[0]: next item, counter[1]: CTAs done
+    uint32_t *flags, *counter;  // counter[0]: next item, counter[1]: CTAs that ask no more
     int batch, Hq, Hkv, cap, n_tokens, max_new, mask_words;
     int g_shift;            // G = 1 << g_shift heads per group
     int item_bound;         // items of a KV head, at most
@@ -589,6 +589,11 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         emit(q, item, g, 0, tiles, -1);
                     else
                         zero_item(q, item, g);
+                }
+                // the last CTA to ask leaves the counter as it was found
+                if (lane == 0 && atom_add_acq_rel_gpu(p.counter + 1, 1u) == gridDim.x - 1) {
+                    p.counter[0] = 0u;
+                    p.counter[1] = 0u;
                 }
             } else {
                 const int cta = blockIdx.x;
@@ -1278,13 +1283,6 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
-    }
-    if (tid == 0 && p.part == nullptr) {
-        // the last CTA to finish leaves the counter as it was found
-        if (atom_add_acq_rel_gpu(p.counter + 1, 1u) == gridDim.x - 1) {
-            p.counter[0] = 0u;
-            p.counter[1] = 0u;
-        }
     }
 }
 
