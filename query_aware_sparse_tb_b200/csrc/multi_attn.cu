@@ -380,17 +380,18 @@ __device__ __forceinline__ int tile_units(const Params &p, const Seq &q, int ite
     const bool pair = min(kItemRows >> p.g_shift, q.kept - item * (kItemRows >> p.g_shift)) > (kSlotRows >> p.g_shift);
     return pair ? 7 : 5;
 }
-__device__ __forceinline__ long long item_units(int tiles, int unit) { return tiles > 0 ? (long long)(tiles + 1) * unit : 0; }
+// (32 bits hold the line: the host deals longer ones out by the counter.)
+__device__ __forceinline__ uint32_t item_units(int tiles, int unit) { return tiles > 0 ? (uint32_t)(tiles + 1) * unit : 0u; }
 // The first tile that begins at or behind unit x of an item.
-__device__ __forceinline__ int tile_behind(long long x, int unit) {
-    return x <= 0 ? 0 : (int)max(1LL, (x + unit - 1) / unit - 1);
+__device__ __forceinline__ int tile_behind(uint32_t x, uint32_t unit) {
+    return x == 0 ? 0 : max(1, (int)((x + unit - 1) / unit) - 1);
 }
 // One sequence's part of the line.
-__device__ __forceinline__ long long seq_units(const Params &p, const Seq &q) {
+__device__ __forceinline__ uint32_t seq_units(const Params &p, const Seq &q) {
     const int items = items_of(p, q.kept);
     if (items == 0) return 0;
     const int base = q.T - q.n, last = items - 1;
-    long long t = item_units(item_tiles(p, q, last), tile_units(p, q, last));
+    uint32_t t = item_units(item_tiles(p, q, last), tile_units(p, q, last));
     if (last > 0) {  // the full items
         const int unit = tile_units(p, q, 0);
         if (p.mask) {
@@ -401,30 +402,30 @@ __device__ __forceinline__ long long seq_units(const Params &p, const Seq &q) {
             // sum of ceil((base + i tpi) / 128) over i = 1 .. last: every `k`
             // items (k = 128 / tpi) the tiles grow by `d`
             const int tpi = kItemRows >> p.g_shift, k = max(1, kTile / tpi), d = max(1, tpi / kTile);
-            const long long blocks = last / k;
-            long long tiles = 0;
+            const int blocks = last / k;
+            int tiles = 0;
             for (int r = 1; r <= k; ++r) {  // i = r, r + k, ..: `count` of them
-                const long long count = blocks + (r <= last % k);
+                const int count = blocks + (r <= last % k);
                 tiles += count * ((base + r * tpi + kTile - 1) / kTile) + d * (count * (count - 1) / 2);
             }
-            t += (tiles + last) * unit;
+            t += (uint32_t)(tiles + last) * unit;
         }
     }
     return t * p.Hkv;
 }
 // The line in `ctas` shares that differ by one unit at most.
 struct Shares {
-    long long total, each;
+    uint32_t total, each;
     int rest, ctas;
-    __device__ __forceinline__ Shares(long long units, int grid) : total(units) {
+    __device__ __forceinline__ Shares(uint32_t units, int grid) : total(units) {
         // no share is below 4 tiles: short contexts keep to fewer CTAs
-        ctas = (int)min((long long)grid, max(1LL, units >> 5));
+        ctas = max(1, min(grid, (int)(units >> 5)));
         each = units / ctas;
         rest = (int)(units - each * ctas);
     }
-    __device__ __forceinline__ long long begin(int c) const { return c >= ctas ? total : each * c + min(c, rest); }
-    __device__ __forceinline__ int holding(long long u) const {  // the share with unit u
-        const long long big = (each + 1) * rest;
+    __device__ __forceinline__ uint32_t begin(int c) const { return c >= ctas ? total : each * c + min(c, rest); }
+    __device__ __forceinline__ int holding(uint32_t u) const {  // the share with unit u
+        const uint32_t big = (each + 1) * rest;
         return (int)(u < big ? u / (each + 1) : rest + (u - big) / each);
     }
 };
@@ -598,9 +599,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             } else {
                 const int cta = blockIdx.x;
                 const Seq seq0 = load_seq(p, lane);  // of the first 32 sequences
-                const long long units0 = warp_prefix(p, seq_units(p, seq0), lane);
+                const uint32_t units0 = warp_prefix(p, seq_units(p, seq0), lane);
                 const int items0 = warp_prefix(p, items_of(p, seq0.kept), lane);
-                long long total = __shfl_sync(kFullMask, units0, 31);
+                uint32_t total = __shfl_sync(kFullMask, units0, 31);
                 int total_items = __shfl_sync(kFullMask, items0, 31);
                 for (int b0 = 32; b0 < p.batch; b0 += 32) {
                     const Seq mine = load_seq(p, b0 + lane);
@@ -609,8 +610,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
                 total_items *= p.Hkv;
                 const Shares sh(total, gridDim.x);
-                long long w = sh.begin(cta);
-                const long long w1 = sh.begin(cta + 1);
+                uint32_t w = sh.begin(cta);
+                const uint32_t w1 = sh.begin(cta + 1);
                 // an entry for every item, or where there are more items than
                 // CTAs, for every CTA (one item at most ends in it that began earlier)
                 const bool by_item = p.item_bound * p.Hkv <= (int)gridDim.x;
@@ -620,12 +621,12 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 };
                 bool joined = false;
                 // the sequence that holds unit w: `at` is where its part of the line begins
-                long long at = 0;
+                uint32_t at = 0;
                 int b = p.batch, items_before = 0;
                 Seq q;
                 for (int b0 = 0; w < w1 && b0 < p.batch; b0 += 32) {
                     const Seq mine = b0 == 0 ? seq0 : load_seq(p, b0 + lane);
-                    const long long incl = b0 == 0 ? units0 : warp_prefix(p, seq_units(p, mine), lane);
+                    const uint32_t incl = b0 == 0 ? units0 : warp_prefix(p, seq_units(p, mine), lane);
                     const int before = b0 == 0 ? items0 : warp_prefix(p, items_of(p, mine.kept), lane);
                     const uint32_t hit = __ballot_sync(kFullMask, w < at + incl);
                     if (hit) {
@@ -643,7 +644,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     const int items = items_of(p, q.kept);
                     for (int i = 0; i < items && ok && w < w1; ++i) {
                         const int tiles = item_tiles(p, q, i), unit = tile_units(p, q, i);
-                        const long long len = item_units(tiles, unit);
+                        const uint32_t len = item_units(tiles, unit);
                         if (w >= at + len * p.Hkv) {
                             at += len * p.Hkv;
                             continue;
@@ -1437,6 +1438,7 @@ bool use_shares(const tb_dims &d, int32_t max_new, bool tree, long long items) {
     const double longest = (d.ctx_cap + kTile - 1) / kTile;
     const double shortest = tree ? longest : fmax(1.0, (double)(d.ctx_cap - max_new) / kTile);
     const double average = 0.5 * (longest + shortest);
+    if (n * (longest + 1.0) * 7.0 >= 2147483648.0) return false;  // (positions on the line are 32 bits)
     const double whole = fmax(longest, n * average / ctas + 0.5 * shortest);
     return n * average / ctas + 16.0 < whole;
 }

@@ -140,6 +140,28 @@ norm_rope_append_kernel(const RopeParams p) {
     if (tok >= p.n_tokens) return;
     const int h0 = (w - tok * warps_per_token) * p.heads_per_warp;
     const int h1 = min(h0 + p.heads_per_warp, heads);
+
+    // this lane's two groups of 4 values: half style pairs group r with group
+    // r + R (R = rot / 8) and leaves the groups from 2 R on alone
+    const int l = lane % LPH, hl = lane / LPH, R = p.rot / 8;
+    const int ga = INTER ? 2 * l : l < R ? l : l + R;
+    const int gb = INTER ? 2 * l + 1 : l < R ? l + R : l + LPH;
+    const uint2 *src = reinterpret_cast<const uint2 *>(p.qkv + (size_t)tok * p.row_stride);
+    uint2 ua[kUnroll], ub[kUnroll];
+    auto fetch = [&](int h, int he) {  // rows h, h + HPI, .. below he
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            ua[u] = ub[u] = make_uint2(0u, 0u);
+            if (h + u * HPI < he) {
+                const uint2 *r = src + (uint32_t)((h + u * HPI) * (D / 4));
+                ua[u] = r[ga];
+                ub[u] = r[gb];
+            }
+        }
+    };
+    // the first rows are on their way while the sequence is looked up
+    fetch(h0 + hl, min(h1, h0 < p.Hq ? p.Hq : h0 < p.Hq + p.Hkv ? p.Hq + p.Hkv : heads));
+
     const int b = find_seq(p.q_begin, p.batch, tok, lane);
     if (b < 0) return;
     const SeqSpan sp = seq_span(p.q_begin, b, p.n_tokens);
@@ -148,11 +170,6 @@ norm_rope_append_kernel(const RopeParams p) {
     const bool cached = row >= 0 && row < p.cap;
     if (!cached && h0 == 0 && lane == 0) raise_flag(p.flags, TB_FLAG_CTX_RANGE);
 
-    // this lane's two groups of 4 values: half style pairs group r with group
-    // r + R (R = rot / 8) and leaves the groups from 2 R on alone
-    const int l = lane % LPH, hl = lane / LPH, R = p.rot / 8;
-    const int ga = INTER ? 2 * l : l < R ? l : l + R;
-    const int gb = INTER ? 2 * l + 1 : l < R ? l + R : l + LPH;
     // which of the lane's pairs turn (rot is a multiple of 8, so in half style
     // all or none, in interleaved style those of a group alike)
     const bool ra = INTER ? ga * 4 < p.rot : l < R, rb = INTER ? gb * 4 < p.rot : l < R;
@@ -181,7 +198,6 @@ norm_rope_append_kernel(const RopeParams p) {
 
     // the heads in three runs: queries, keys, values; in each kUnroll rows a
     // lane are requested before the first is worked on
-    const uint2 *src = reinterpret_cast<const uint2 *>(p.qkv + (size_t)tok * p.row_stride);
     auto run = [&](int begin, int end, uint16_t *out, uint32_t step, auto turn_c, const uint16_t *weight) {
         constexpr bool kTurn = decltype(turn_c)::value;
         const int hb = max(begin, h0), he = min(end, h1);
@@ -193,16 +209,7 @@ norm_rope_append_kernel(const RopeParams p) {
         }
         uint2 *dst = reinterpret_cast<uint2 *>(out);
         for (int h = hb + hl; h - hl < he; h += HPI * kUnroll) {
-            uint2 ua[kUnroll], ub[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                ua[u] = ub[u] = make_uint2(0u, 0u);
-                if (h + u * HPI < he) {
-                    const uint2 *r = src + (uint32_t)((h + u * HPI) * (D / 4));
-                    ua[u] = r[ga];
-                    ub[u] = r[gb];
-                }
-            }
+            if (h != h0 + hl) fetch(h, he);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 if (h - hl + u * HPI >= he) break;  // (the same for all lanes)
