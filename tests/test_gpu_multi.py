@@ -158,6 +158,14 @@ def test_prompt_group_sizes(G):
     check(out[:sum(n)], ref[:sum(n)], tol[:sum(n)], f"G={G}")
 
 
+@pytest.mark.parametrize("cap,T", [(1, 1), (2, 2), (5, 4), (127, 127), (129, 129)])
+def test_caches_smaller_than_a_tile_and_of_odd_size(cap, T):
+    for n in (1, T):
+        Q, K, V, out, scale = run_prompt([n], [T], 1, 1, 64, seed=cap, cap=cap)
+        ref, tol = reference(Q, K, V, [n], [T], scale, causal([n], [T]))
+        check(out[:n], ref[:n], tol[:n], f"cap {cap}, n {n}")
+
+
 def test_prompt_long_covers_every_wave():
     n, T = [2500, 700], [2500, 1300]
     Q, K, V, out, scale = run_prompt(n, T, 32, 8, 128, seed=3)
@@ -230,6 +238,16 @@ def test_tree(n, T, d):
     Q, K, V, out, scale = run_tree(n, T, masks, 8, 2, d)
     ref, tol = reference(Q, K, V, n, T, scale, tree_see(masks, n, T))
     check(out[:sum(n)], ref[:sum(n)], tol[:sum(n)], f"{n}")
+
+
+@pytest.mark.parametrize("G", [1, 2, 8, 16])
+def test_tree_group_sizes(G):
+    n, T = [33, 1, 20], [600, 40, 20]
+    r = np.random.RandomState(G)
+    masks = [random_tree(k, r) for k in n]
+    Q, K, V, out, scale = run_tree(n, T, masks, 2 * G, 2, 64, seed=G)
+    ref, tol = reference(Q, K, V, n, T, scale, tree_see(masks, n, T))
+    check(out[:54], ref[:54], tol[:54], f"G={G}")
 
 
 def test_tree_any_mask_and_rows_that_see_nothing():
