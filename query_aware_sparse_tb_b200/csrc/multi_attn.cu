@@ -50,8 +50,8 @@
 //   - 64 head dims: the softmax (the products are half as long, the
 //     exponentials as many): 735 TFLOP/s at 8K tokens.
 //   - trees and decode steps over long contexts: HBM.  26 drafted tokens over
-//     64K rows stream 269 MB in 37 of 56 us; the rest is the start (5 us), the
-//     states (3 us) and their join (5 us).
+//     64K rows take 58 us in a graph.  37 of them stream 269 MB; the rest is
+//     the launches, the start (5 us), the states (3 us) and their join (5 us).
 #include <cuda.h>
 #include <math.h>
 
@@ -434,7 +434,8 @@ struct Shares {
 // sequences or of nobody.  Where they are a quarter or more, warp 11 clears
 // them before the products use them: products with zeros draw less power, and
 // power is what bounds the clock (16 ragged trees: 415 -> 391 us; the look at
-// the queries costs about 0.4 us an item).
+// the queries costs about 0.4 us an item: 16 trees over 16K, items of 64 tokens,
+// 33 of them live: 286 us without, 272 with; 48 live: 291, 285; 60 live: 300, 297).
 __device__ __forceinline__ bool many_dead(int live, int rows) { return 4 * (rows - live) >= rows; }
 
 template <int D>
@@ -1148,8 +1149,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
-                        // rounded to bf16 for the second product: 2^-9 relative
-                        // per weight, below the rounding of the bf16 result
+                        // rounded to bf16 for the second product: at most 2^-8
+                        // relative per weight, as the rounding of the result,
+                        // and of either sign, so a row's errors mostly cancel
                         w[i] = pack_bf16(e0, e1);
                     }
                     tmem_st16(tp + q * 16, w);
@@ -1465,6 +1467,8 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
     if (e != cudaSuccess || !p.part) return e;
     const dim3 grid(items < sms ? (unsigned)items : ctas, kItemRows / 32, D / 32);
     // about sms / items states an item: above 6, 4 groups of warps read them
+    // (trees over 32K, both kernels: 8 items 39.4 us with one group, 36.1 with
+    // four; 16 items 58.8, 59.0; 32 items 98, 104)
     if (sms > 6 * items) return launch_pdl(multi_join_kernel<D, 4>, grid, dim3(512), 0, st, p);
     return launch_pdl(multi_join_kernel<D, 1>, grid, dim3(128), 0, st, p);
 }

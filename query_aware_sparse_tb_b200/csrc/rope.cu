@@ -18,6 +18,9 @@
 // values that pair up within the lane, so the rotation needs no exchange and
 // the norm one reduction over the lanes.  A lane keeps the 4 (cos, sin) pairs
 // of its values in registers for all of the token's heads.
+//
+// On a B200, 32 query and 8 KV heads of 128: 32K tokens (805 MB moved) 127 us
+// in a graph, 6.34 TB/s or 0.97 of a plain copy; 16 tokens 3.1 us, the launch.
 #include "common.cuh"
 #include "internal.h"
 #include "multi.h"
@@ -288,10 +291,13 @@ cudaError_t launch_norm_rope_append(const tb_dims &d, const uint16_t *qkv, int64
     p.rot = rot_dim;
     p.interleaved = style == TB_ROPE_INTERLEAVED;
     // a warp takes all of a token's heads (its angles are worked out once)
-    // unless that leaves SMs idle; then one unrolled round of heads each
+    // unless that leaves SMs idle; then one unrolled round of heads each.  With
+    // 48 heads of 128: 64 tokens 7.2 us whole, 3.1 in rounds; 2,368: 16.7, 15.4;
+    // 2,800: 17.4, 17.5; 3,500: 18.7, 20.8; 8,000: 35.4, 41.8.  The two meet
+    // between 2,700 and 3,000 tokens for 24 to 80 heads of 64 or 128.
     const int heads = d.n_q_heads + 2 * d.n_kv_heads;
     const int round = 4 * (32 / (d.head_dim / 8));
-    p.heads_per_warp = n_tokens >= num_sms() * 16 ? heads : round;
+    p.heads_per_warp = n_tokens >= num_sms() * 19 ? heads : round;
     const long long warps = (long long)n_tokens * ((heads + p.heads_per_warp - 1) / p.heads_per_warp);
     const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     auto *kernel = d.head_dim == 128 ? (p.interleaved ? norm_rope_append_kernel<128, true> : norm_rope_append_kernel<128, false>)
