@@ -506,6 +506,77 @@ def test_prompt_is_deterministic_and_replays_in_a_graph():
     assert tb.workspace_check(ws) == 0
 
 
+@pytest.mark.parametrize("d,hkv,cap", [(128, 2, 4096), (64, 8, 512)])  # equal shares of the tiles; whole items
+def test_a_captured_drafting_step_follows_lengths_and_masks(d, hkv, cap):
+    """Norm + rotation, tree attention and acceptance captured once, replayed
+    with other sequence starts, lengths, positions, masks and paths."""
+    B, hq, tokens, mn = 8, 4 * hkv, 120, 40
+    dm = tb.dims(B, hq, hkv, d, 16, cap)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    first = torch.randn(2, B, hkv, cap, d, generator=g, device=DEV).to(torch.bfloat16)
+    inv = 10000.0 ** (-2 * torch.arange(d // 2, dtype=F64, device=DEV) / d)
+    words = (mn + 31) // 32
+
+    def inputs(seed):
+        r = np.random.RandomState(seed)
+        n = [0] * B
+        for _ in range(tokens - 5 * seed):  # some of the buffers' tokens belong to nobody
+            n[r.choice([b for b in range(B) if n[b] < mn])] += 1
+        T = [k + int(r.randint(0, cap - k + 1)) for k in n]
+        masks = [random_tree(k, r) if k else np.zeros((0, 0), bool) for k in n]
+        mask = torch.zeros(tokens, words, dtype=torch.int32, device=DEV)
+        rows = pack_rows([row for m in masks for row in m], words)
+        mask[:rows.shape[0]] = rows
+        path, plen = np.zeros((B, mn), np.int32), [0] * B
+        for b in range(B):
+            if n[b]:
+                kept = np.flatnonzero(masks[b][int(r.randint(n[b]))])
+                plen[b] = len(kept)
+                path[b, :plen[b]] = kept
+        pos = i32(r.randint(0, 100000, tokens).tolist())
+        gg = torch.Generator(device=DEV).manual_seed(100 + seed)
+        qkv = torch.randn(tokens, (hq + 2 * hkv) * d, generator=gg, device=DEV).to(torch.bfloat16)
+        return [i32(starts(n)), i32(T), pos, mask, i32(path), i32(plen), qkv]
+
+    def buffers():
+        kv = first.clone()
+        return dict(kv=kv, caches=torch.tensor([kv[0].data_ptr(), kv[1].data_ptr()], dtype=torch.int64, device=DEV),
+                    Q=torch.zeros(tokens, hq, d, dtype=torch.bfloat16, device=DEV),
+                    out=torch.zeros(tokens, hq, d, dtype=torch.bfloat16, device=DEV),
+                    new_len=torch.zeros(B, dtype=torch.int32, device=DEV), ws=tb.workspace(256),
+                    wt=tb.workspace(tb.tree_attn_workspace_bytes(dm, tokens, mn)))
+
+    def step(x, y):
+        qb, T, pos, mask, path, plen, qkv = x
+        K, V = y["kv"][0], y["kv"][1]
+        tb.norm_rope_append(dm, qkv, qb, T, pos, None, None, 0.0, inv, True, y["Q"], K, V, y["ws"])
+        tb.tree_attn(dm, y["Q"], K, V, qb, mn, T, mask, 1 / math.sqrt(d), y["out"], y["wt"])
+        tb.tree_accept(dm, 1, y["caches"], qb, T, path, plen, y["new_len"], y["ws"])
+
+    x, y = inputs(0), buffers()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            step(x, y)
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in (3, 0, 7):
+        new, want = inputs(seed), buffers()
+        step(new, want)
+        for a, b in zip(x, new):
+            a.copy_(b)
+        y["kv"].copy_(first)
+        for name in ("Q", "out", "new_len"):
+            y[name].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("kv", "Q", "out", "new_len"):
+            assert torch.equal(y[name], want[name]), (seed, name)
+        for w in (y["ws"], y["wt"], want["ws"], want["wt"]):
+            assert tb.workspace_check(w) == 0
+        assert bool((want["new_len"] <= new[1]).all()) and not bool((want["out"] == 0).all())
+
+
 # ------------------------------------------------------------------ a run of them together
 
 def test_prompt_tree_accept_decode_together():
