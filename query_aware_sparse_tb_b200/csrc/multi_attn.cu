@@ -560,6 +560,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     f[kTiles1] = pair ? nt : nt / 2;
                     f[kMaskLo] = p.mask ? q.T - q.n : q.T - q.n + tok0 + 1;
                     f[kPart] = part;
+                    // no V row taken out yet: seg_full hands that to every
+                    // role, those that no tile orders behind warp 11 too
+                    *reinterpret_cast<volatile int *>(sm + L::kBad + (k & 1) * kBadBytes) = 0;
                     mbar_arrive(seg_full(k & 1));
                 }
                 __syncwarp();
@@ -789,8 +792,6 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 const int nt = f[kTiles], ahead = (f[kPair] ? 0 : 1) + (L::kSepP ? 1 : 0);
                 const int row0 = f[kFirst] * kTile, mask_lo = f[kMaskLo] - row0, len = f[kLen] - row0;
                 volatile int *bad = reinterpret_cast<volatile int *>(sm + L::kBad + (k & 1) * kBadBytes);
-                if (lane == 0) bad[0] = 0;
-                __syncwarp();
                 const int live = f[kNTok] << p.g_shift, rows = f[kPair] ? kItemRows : kSlotRows;
                 if (many_dead(live, rows)) {
                     ok = wait_warp(q_raw, raws & 1, abort_flag, p.flags);
@@ -851,6 +852,9 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                             if (lane == 0 && n_bad < kMaxMasked) bad[2 + 5 * n_bad + q] = (int)w;
                         }
                         n_bad = min(n_bad + 1, kMaxMasked);
+                        // (a pair's first slot may read the list meanwhile: the
+                        // entry before its count)
+                        __threadfence_block();
                         if (lane == 0) bad[0] = n_bad;
                         wrote = true;
                     }
@@ -1212,7 +1216,10 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             uint16_t *dst = p.out + ((size_t)(f[kTok] + ti) * p.Hq + h) * D;
             float *part = p.part + (size_t)max(part_slot, 0) * ((D + 2) * kItemRows) + (pair ? slot : 0) * kSlotRows + row;
             volatile const int *bad = reinterpret_cast<volatile const int *>(sm + L::kBad + (k & 1) * kBadBytes);
-            const int n_bad = bad[0];
+            // (the tiles this slot used are in the list: their products waited
+            // for warp 11; further ones may come in, for rows it does not see)
+            const int n_bad = n_mine > 0 || !pair ? bad[0] : 0;
+            if (n_bad > 0) __threadfence_block();
             const int q0 = pair ? 0 : slot * (D / 32), q1 = pair ? D / 16 : q0 + D / 32;  // groups of 16 head dims
 #pragma unroll 1
             for (int q = q0; q < q1; ++q) {

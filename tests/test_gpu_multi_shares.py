@@ -1,0 +1,74 @@
+"""Prompt and tree attention where the work is dealt out in equal shares of all
+tiles, at shapes named by what they reach in that rule (tests/multi_dealing.py
+restates it), against the 64-bit reference and tolerance of test_gpu_multi."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import query_aware_sparse_tb_b200 as tb
+import test_gpu_multi as multi
+from multi_dealing import Dealing
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def fill_shared_memory():
+    """A matrix product whose operand tiles stay behind in the SMs' shared memory."""
+    a = torch.full((2048, 2048), 3.0, dtype=torch.bfloat16, device=DEV)
+    return a @ a
+
+
+def run(n, T, hkv, G, d, tree, cap=None, seed=0, repeats=1, before=None, K=None, V=None):
+    hq = hkv * G
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    cap = cap or (max(T) + 127) // 128 * 128
+    if K is None:
+        K, V = multi.make_cache(g, len(n), hkv, cap, d, T)
+    total = sum(n)
+    Q = torch.randn(total + 2, hq, d, generator=g, device=DEV).to(torch.bfloat16)
+    dm, mx = tb.dims(len(n), hq, hkv, d, 16, cap), max(n)
+    scale = 1 / math.sqrt(d)
+    size = (tb.tree_attn_workspace_bytes if tree else tb.prompt_attn_workspace_bytes)(dm, total + 2, mx)
+    assert size > 1 << 20, "whole items, not shares"
+    ws, qb, ctx = tb.workspace(size), multi.i32(multi.starts(n)), multi.i32(T)
+    masks = mask = None
+    if tree:
+        r = np.random.RandomState(seed)
+        masks = [multi.random_tree(k, r) for k in n]
+        words = (mx + 31) // 32
+        mask = torch.cat([multi.pack_rows([row for m in masks for row in m], words),
+                          torch.zeros(2, words, dtype=torch.int32, device=DEV)])
+    outs = []
+    for _ in range(repeats):
+        out = torch.full((total + 2, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        if before:
+            before()
+        if tree:
+            tb.tree_attn(dm, Q, K, V, qb, mx, ctx, mask, scale, out, ws)
+        else:
+            tb.prompt_attn(dm, Q, K, V, qb, mx, ctx, scale, out, ws)
+        assert tb.workspace_check(ws) == 0
+        assert (out[total:] == 7).all()
+        outs.append(out[:total])
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    see = multi.tree_see(masks, n, T) if tree else multi.causal(n, T)
+    ref, tol = multi.reference(Q[:total], K, V, n, T, scale, see)
+    multi.check(outs[0], ref, tol, f"{n} {T}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,T,hkv,G", [
+    ([200], [3225], 32, 1),
+    ([200], [3250], 32, 1),
+    ([300] * 4, [4300] * 4, 8, 4),
+    ([300] * 4, [9400] * 4, 8, 4),
+])
+def test_a_share_that_begins_behind_the_first_slots_tokens(n, T, hkv, G, d):
+    """A CTA's first segment of two row blocks may hold only tiles that the
+    first block does not see; whatever shared memory held before must not
+    matter to it."""
+    assert Dealing(n, T, hkv, G, False).check().slot0_without_tiles() > 0
+    run(n, T, hkv, G, d, False, cap=12288, seed=3, repeats=3, before=fill_shared_memory)
