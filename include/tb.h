@@ -492,7 +492,8 @@ tb_status tb_sparse_decode_attn_noalloc(const tb_dims *dims, const tb_bf16 *Q, c
  *
  * Tokens are packed: sequence b's are tokens q_begin[b] .. q_begin[b+1] of
  * the packed arrays (q_begin: [batch + 1] int32, device, rising from 0; a
- * sequence may have none), n_tokens (host) is the packed arrays' token count;
+ * sequence may have none; one that does not rise gives any result, but no
+ * access outside the arrays), n_tokens (host) is the packed arrays' token count;
  * tokens at or past q_begin[batch] take no part and nothing is written for them.  n =
  * q_begin[b+1] - q_begin[b] and T = ctx_len[b], which counts the new tokens:
  * token i of sequence b sits at cache row T - n + i.  A sequence with n = 0

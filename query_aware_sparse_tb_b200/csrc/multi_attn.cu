@@ -619,7 +619,10 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 // an entry for every item, or where there are more items than
                 // CTAs, for every CTA (one item at most ends in it that began earlier)
                 const bool by_item = p.item_bound * p.Hkv <= (int)gridDim.x;
+                // (a q_begin that does not rise may give more items than the host's
+                // bound: what is behind the list is not written)
                 auto join = [&](int entry, int from, int tok, int head, int rows) {
+                    if (entry >= (int)gridDim.x) return;
                     if (lane == 0) *reinterpret_cast<int4 *>(p.joins + 8 * entry) = make_int4(from, cta - from + 1, tok, head);
                     if (lane == 0) p.joins[8 * entry + 4] = rows;
                 };

@@ -72,3 +72,23 @@ def test_a_share_that_begins_behind_the_first_slots_tokens(n, T, hkv, G, d):
     matter to it."""
     assert Dealing(n, T, hkv, G, False).check().slot0_without_tiles() > 0
     run(n, T, hkv, G, d, False, cap=12288, seed=3, repeats=3, before=fill_shared_memory)
+
+
+def test_a_q_begin_that_does_not_rise_stays_in_the_join_list():
+    """Overlapping sequences are more items than the host's bound.  Entries past
+    the list of join entries would begin to overwrite state 0, which no CTA
+    writes (nothing begins before the first share)."""
+    B, tokens, d, cap, sms = 100, 300, 64, 16384, torch.cuda.get_device_properties(0).multi_processor_count
+    with pytest.raises(AssertionError, match="list not written whole"):
+        Dealing([tokens, 0] * (B // 2), [600] * B, 1, 4, False, n_tokens=tokens, ctas=sms).check()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    K, V = multi.make_cache(g, B, 1, cap, d, [600] * B)
+    Q = torch.randn(tokens, 4, d, generator=g, device=DEV).to(torch.bfloat16)
+    out, dm = torch.zeros_like(Q), tb.dims(B, 4, 1, d, 16, cap)
+    ws = tb.workspace(tb.prompt_attn_workspace_bytes(dm, tokens, tokens))
+    assert ws.numel() > 1 << 20
+    ws[256:] = 0xA5
+    tb.prompt_attn(dm, Q, K, V, multi.i32([0, tokens] * (B // 2) + [0]), tokens, multi.i32([600] * B), 0.125, out, ws)
+    torch.cuda.synchronize()
+    states = 2 * sms * (d + 2) * 256 * 4
+    assert (ws[-states:][:(d + 2) * 256 * 4] == 0xA5).all()
