@@ -547,6 +547,7 @@ tb_status tb_norm_rope_append(const tb_dims *dims, const tb_bf16 *qkv, int64_t r
  * With T = n this is a whole prompt; with T > n, a chunk behind cached rows;
  * with n = 1 the decode step.  fp32 logits, softmax statistics and sums; the
  * weights are rounded to bf16 for the product with V, the result to bf16.
+ * A logit that, times log2(e), is past fp32's range makes its row NaN.
  * Cache rows at or past T cannot reach the result, whatever they hold.  A
  * ctx_len outside [1, ctx_cap] is clamped and one smaller than n leaves the
  * first tokens without a row (their result is 0); both raise
