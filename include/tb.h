@@ -40,7 +40,14 @@
  *    with tb_workspace_check().
  *  - Workspaces must be zeroed once before first use (tb_workspace_init); every
  *    call leaves its counters and histograms zeroed again.  Two calls that use
- *    the same workspace must not overlap on the device.
+ *    the same workspace must not overlap on the device.  A workspace belongs to
+ *    one kind of call (the selection calls, tb_predict_queries, the attention
+ *    calls) and one set of dims: each leaves intermediate values where another
+ *    keeps its counters, so initialise it again before another uses it.  The
+ *    decode attention calls, tb_prompt_attn and tb_tree_attn may take turns on
+ *    one workspace of the largest of their sizes if batch and n_kv_heads are
+ *    the same.  Calls that ask for 256 bytes use the flag word only: any
+ *    workspace does for them.
  */
 #ifndef TB_H
 #define TB_H

@@ -1505,11 +1505,16 @@ cudaError_t launch_d(const tb_dims &d, const uint16_t *Q, const uint16_t *K, con
 
 }  // namespace
 
-// Workspace: flag word, counter (at 64), the CTAs' join entries, their states.
+// Workspace: flag word, counter (at 64), a word for each (sequence, KV head) that
+// is left alone, the CTAs' join entries, their states.  The words are the decode
+// attention's tickets, which have to be zero between calls: a program that
+// verifies a tree and then decodes may use one workspace for both.
+size_t joins_at(const tb_dims &d) { return kWsHeaderBytes + align_up((size_t)d.batch * d.n_kv_heads * 4, 256); }
+size_t states_at(const tb_dims &d) { return joins_at(d) + align_up((size_t)num_sms() * 32, 256); }
+
 size_t multi_attn_ws_bytes(const tb_dims &d, int32_t n_tokens, int32_t max_new, bool tree) {
     if (!use_shares(d, max_new, tree, item_bound(d, n_tokens, max_new))) return kWsHeaderBytes;
-    const size_t ctas = (size_t)num_sms();
-    return kWsHeaderBytes + align_up(ctas * 32, 256) + ctas * 2 * (d.head_dim + 2) * kItemRows * sizeof(float);
+    return states_at(d) + (size_t)num_sms() * 2 * (d.head_dim + 2) * kItemRows * sizeof(float);
 }
 
 cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
@@ -1536,8 +1541,8 @@ cudaError_t launch_multi_attn(const tb_dims &d, const uint16_t *Q, const uint16_
     p.g_shift = log2_int(d.n_q_heads / d.n_kv_heads);
     p.item_bound = (int)item_bound(d, n_tokens, max_new);
     if (use_shares(d, max_new, mask != nullptr, p.item_bound)) {
-        p.joins = reinterpret_cast<int32_t *>(w + kWsHeaderBytes);
-        p.part = reinterpret_cast<float *>(w + kWsHeaderBytes + align_up((size_t)num_sms() * 32, 256));
+        p.joins = reinterpret_cast<int32_t *>(w + joins_at(d));
+        p.part = reinterpret_cast<float *>(w + states_at(d));
     }
     p.c = scale * 1.4426950408889634f;
     return d.head_dim == 128 ? launch_d<128>(d, Q, K, V, p, st) : launch_d<64>(d, Q, K, V, p, st);

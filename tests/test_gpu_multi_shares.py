@@ -92,3 +92,43 @@ def test_a_q_begin_that_does_not_rise_stays_in_the_join_list():
     torch.cuda.synchronize()
     states = 2 * sms * (d + 2) * 256 * 4
     assert (ws[-states:][:(d + 2) * 256 * 4] == 0xA5).all()
+
+
+def test_decode_attention_takes_turns_on_the_workspace():
+    """Verification and the decode step behind it on one workspace: the states
+    of the shares must not lie where the decode attention keeps its tickets."""
+    B, hkv, d, cap = 3, 2, 128, 8192
+    n, T = [20, 9, 1], [5000, 3000, 7000]
+    g = torch.Generator(device=DEV).manual_seed(4)
+    K, V = multi.make_cache(g, B, hkv, cap, d, T)
+    dm, scale = tb.dims(B, 4 * hkv, hkv, d, 16, cap), 1 / math.sqrt(d)
+    Q = torch.randn(30, 4 * hkv, d, generator=g, device=DEV).to(torch.bfloat16)
+    last = Q[[19, 28, 29]].contiguous()
+    r = np.random.RandomState(4)
+    mask = multi.pack_rows([row for k in n for row in multi.random_tree(k, r)], 1)
+    qb, ctx = multi.i32(multi.starts(n)), multi.i32(T)
+    sizes = [tb.tree_attn_workspace_bytes(dm, 30, 20), tb.prompt_attn_workspace_bytes(dm, 30, 20),
+             tb.attn_workspace_bytes(dm)]
+    assert min(sizes[:2]) > 1 << 20
+
+    def tree(ws):
+        out = torch.zeros_like(Q)
+        tb.tree_attn(dm, Q, K, V, qb, 20, ctx, mask, scale, out, ws)
+        return out
+
+    def prompt(ws):
+        out = torch.zeros_like(Q)
+        tb.prompt_attn(dm, Q, K, V, qb, 20, ctx, scale, out, ws)
+        return out
+
+    def decode(ws):
+        out = torch.zeros(B, 4 * hkv, d, device=DEV)
+        tb.decode_attn(dm, last, K, V, ctx, scale, out, ws)
+        return out
+
+    calls = [tree, prompt, decode]
+    want = [f(tb.workspace(size)) for f, size in zip(calls, sizes)]
+    shared = tb.workspace(max(sizes))
+    for k in (0, 2, 1, 2, 2, 0, 1, 2):
+        assert torch.equal(calls[k](shared), want[k]), calls[k].__name__
+    assert tb.workspace_check(shared) == 0
