@@ -152,7 +152,8 @@ int rope(PyObject *const *a) {
     }
     const int inter = PyObject_IsTrue(a[9]);
     if (inter < 0) throw Bad{true, ""};
-    return g_rope(&c.dims, static_cast<tb_bf16 *>(qkv.data_ptr()), n > 1 ? qkv.stride(0) : std::max(width, qkv.stride(0)),
+    // (of one token the stride means nothing: it may be any number)
+    return g_rope(&c.dims, static_cast<tb_bf16 *>(qkv.data_ptr()), n > 1 ? qkv.stride(0) : width,
                   c.lengths(a[2], "q_begin", 1), (int32_t)n, c.lengths(a[3], "ctx_len"), pos, c.weight(a[5], "q_weight"),
                   c.weight(a[6], "k_weight"), real(a[7]), inv, (int32_t)(2 * freqs[0]),
                   inter ? TB_ROPE_INTERLEAVED : TB_ROPE_HALF, c.rows(a[10], "Q", n), c.cache(a[11], "K"),
