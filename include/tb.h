@@ -588,7 +588,8 @@ tb_status tb_tree_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, 
  *   path      [batch][path_cap] int32: drafted tokens (index within the
  *             sequence), strictly rising; path_cap <= 1024
  *   path_len  [batch] int32, 0 (nothing accepted) .. n
- *   new_len   [batch] int32 out; must not overlap ctx_len
+ *   new_len   [batch] int32 out; must not overlap an input; a sequence without
+ *             drafted tokens keeps ctx_len[b], whatever that is
  * Rows behind the new length keep what they held.  A path that does not rise
  * or leaves [0, n) moves nothing, keeps new_len[b] = T and raises
  * TB_FLAG_BAD_PATH in ws (>= 256 bytes); so does n outside [0, T] or T above

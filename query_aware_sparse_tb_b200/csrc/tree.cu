@@ -33,7 +33,9 @@ tree_accept_kernel(const uint64_t *__restrict__ caches, const int32_t *__restric
     griddep_launch_dependents();
     const int b = blockIdx.y, cache = blockIdx.x, tid = threadIdx.x;
     const int T = ctx_len[b], n = q_begin[b + 1] - q_begin[b], len = path_len[b];
-    bool bad = n < 0 || n > T || T > cap || T < 0 || len < 0 || len > n || len > path_cap;
+    // (an idle sequence's length may be anything: it comes back as it is)
+    const bool idle = n == 0 && len == 0;
+    bool bad = !idle && (n < 0 || n > T || T > cap || T < 0 || len < 0 || len > n || len > path_cap);
     if (!bad) {
         const int32_t *pb = path + (size_t)b * path_cap;
         for (int j = tid; j < len; j += kThreads) {
