@@ -76,7 +76,7 @@ typedef enum {
 #define TB_FLAG_CTX_RANGE   0x1u  /* some ctx_len[b] outside [1, ctx_cap]: clamped */
 #define TB_FLAG_TIMEOUT     0x2u  /* a bounded wait gave up; the output is invalid */
 #define TB_FLAG_IDX_OVERFLOW 0x4u /* selected set larger than idx_cap: truncated */
-#define TB_FLAG_BAD_CACHE   0x8u  /* tb_kv_append: a cache address was null or misaligned: skipped */
+#define TB_FLAG_BAD_CACHE   0x8u  /* tb_kv_append, tb_tree_accept: a cache address was null or misaligned: skipped */
 #define TB_FLAG_BAD_PATH    0x10u /* tb_tree_accept: a path that does not rise or leaves the drafted rows: skipped */
 
 /* Shapes shared by the cache-facing calls. */
@@ -580,8 +580,8 @@ tb_status tb_tree_attn(const tb_dims *dims, const tb_bf16 *Q, const tb_bf16 *K, 
                        const uint32_t *mask, float scale, tb_bf16 *out, void *ws, size_t ws_bytes, void *stream);
 
 /* Keep the accepted path of each sequence's drafted tree: in every layer's K
- * and V cache (addresses in `caches`, as for tb_kv_append), with T, n as
- * above,
+ * and V cache (addresses in `caches`, as for tb_kv_append; one that is listed
+ * again, by layers that share a cache, is moved once), with T, n as above,
  *
  *   row T - n + j <- row T - n + path[b][j],  j < path_len[b];  new_len[b] = T - n + path_len[b]
  *

@@ -44,13 +44,16 @@ tree_accept_kernel(const uint64_t *__restrict__ caches, const int32_t *__restric
             bad |= v >= n || v < 0 || (j > 0 && pb[j - 1] >= v);
         }
     }
+    // a cache listed again is moved once, by the block of its first entry (the
+    // first entry of all is nobody's repeat, so `bad` stays what the path says)
+    const uint64_t base = caches[cache];
+    for (int j = tid; j < cache; j += kThreads) bad |= caches[j] == base;
     bad = __syncthreads_or(bad);
     if (tid == 0 && cache == 0) {
         if (bad) raise_flag(flags, TB_FLAG_BAD_PATH);
         new_len[b] = bad ? T : T - n + len;
     }
     if (bad) return;
-    const uint64_t base = caches[cache];
     if (base == 0 || (base & 15u) != 0) {
         if (tid == 0) raise_flag(flags, TB_FLAG_BAD_CACHE);
         return;

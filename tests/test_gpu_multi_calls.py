@@ -53,3 +53,17 @@ def test_accept_does_not_look_at_idle_sequences():
                                            lambda a: [x for pair in a for x in pair])
     assert flags == 0 and new_len == [18, -1, 0, 1 << 30, 7]
     assert torch.equal(kv, want)
+
+
+@pytest.mark.parametrize("caches_of", [
+    lambda a: [x for pair in a for x in pair] + a[1],                 # a layer that reads another's cache
+    lambda a: [a[0][0], a[0][0], a[0][1], a[0][1]] + a[1] + a[2],     # K and V one array
+    lambda a: (a[0] + a[1] + a[2]) * 40,                              # many times
+])
+def test_accept_moves_a_cache_that_is_listed_twice_once(caches_of):
+    n, T = [26, 40], [50, 64]
+    path = [list(range(1, 26, 2)) + [0] * 8, list(range(19, 40))]
+    for _ in range(5):
+        kv, want, new_len, flags = accept_case([13, 21], n, T, path, caches_of)
+        assert flags == 0 and new_len == [37, 45]
+        assert torch.equal(kv, want)
