@@ -107,15 +107,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "tb_tree_attn": ([D, P, P, P, P, i32, i32, P, P, f32, P, P, sz, P], ctypes.c_int),
         "tb_tree_accept": ([D, i32, P, P, P, P, i32, P, P, P, sz, P], ctypes.c_int),
     }
+    # the signatures above are those of this ABI version; a library built from
+    # other sources would be called with the wrong arguments, or (entry points
+    # have been added within a version) lack some of them
+    rebuild = "rebuild it with `python -m query_aware_sparse_tb_b200.build`"
+    if not hasattr(lib, "tb_abi_version"):
+        raise TbError(-1, f"{path} has no tb_abi_version: {rebuild}")
+    if lib.tb_abi_version() != TB_ABI_VERSION:
+        raise TbError(-1, f"{path} has ABI version {lib.tb_abi_version()}, this binding needs {TB_ABI_VERSION}: {rebuild}")
+    missing = [name for name in sig if not hasattr(lib, name)]
+    if missing:
+        raise TbError(-1, f"{path} was built from older sources and lacks {', '.join(missing)}: {rebuild}")
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
-    # the signatures above are those of this ABI version; a library built from
-    # other sources would be called with the wrong arguments
-    if lib.tb_abi_version() != TB_ABI_VERSION:
-        raise TbError(-1, f"{path} has ABI version {lib.tb_abi_version()}, this binding needs {TB_ABI_VERSION}: "
-                          "rebuild it with `python -m query_aware_sparse_tb_b200.build`")
     if path == LIB_PATH:
         _lib = lib
     return lib
