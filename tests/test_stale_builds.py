@@ -1,11 +1,12 @@
 """Libraries that do not belong to the sources beside them are refused with a
 message that says what to do."""
+import os
 import shutil
 import subprocess
 
 import pytest
 
-from query_aware_sparse_tb_b200 import _lib
+from query_aware_sparse_tb_b200 import _lib, build
 
 
 def c_library(tmp_path, source):
@@ -26,3 +27,32 @@ def c_library(tmp_path, source):
 def test_a_library_of_older_sources_is_refused_with_a_message(tmp_path, source, message):
     with pytest.raises(_lib.TbError, match=message):
         _lib.load(c_library(tmp_path, source))
+
+
+# ------------------------------------------------------------------ the call module
+
+@pytest.fixture
+def compiler(tmp_path, monkeypatch):
+    """build_call() with a compiler that only notes that it was called, into a
+    folder of its own."""
+    runs, script = tmp_path / "runs", tmp_path / "cxx"
+    script.write_text(f'#!/bin/sh\necho "$@" >> {runs}\nwhile [ "$1" != "-o" ]; do shift; done\ntouch "$2"\n')
+    script.chmod(0o755)
+    monkeypatch.setattr(build, "CXX", str(script))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(build, "CALL", str(tmp_path / "_tbcall.so"))
+    return lambda: len(runs.read_text().splitlines()) if runs.exists() else 0
+
+
+def test_the_library_is_built_without_a_cpp_compiler(compiler, monkeypatch):
+    build.build_call()
+    monkeypatch.setattr(build, "CXX", "/no/such/compiler")
+    os.utime(build.CALL, (0, 0))                  # older than its sources
+    with pytest.raises(OSError):
+        build.build_call()
+    assert not os.path.exists(build.CALL)         # the stale one is gone
+    monkeypatch.setattr(build, "SOURCES", [])     # (nothing to compile)
+    monkeypatch.setattr(build, "LIB", os.path.join(build.BUILD, "libtb.so"))
+    open(build.LIB, "w").close()
+    with pytest.warns(UserWarning, match="libtb.so is built, _tbcall.so is not"):
+        assert build.build() == build.LIB
