@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import torch
 
@@ -344,6 +345,11 @@ def kv_append(d: TbDims, n_layers: int, src, caches, ctx_len, ws, stream=None):
 _call = None
 
 
+def call_tag() -> str:
+    """What _tbcall.so is built for: it is bound to torch's and Python's C++ side."""
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
 def _tbcall():
     global _call
     if _call is None:
@@ -353,6 +359,9 @@ def _tbcall():
         except ImportError as e:
             raise TbError(-1, f"_tbcall.so is missing or does not load ({e}): build it with "
                               "`python -m query_aware_sparse_tb_b200.build`") from e
+        if getattr(mod, "built_for", None) != call_tag():
+            raise TbError(-1, f"_tbcall.so was built for {getattr(mod, 'built_for', 'another build')}, this is "
+                              f"{call_tag()}: rebuild it with `python -m query_aware_sparse_tb_b200.build`")
         mod.bind(TbError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.tb_norm_rope_append, lib.tb_prompt_attn, lib.tb_tree_attn, lib.tb_tree_accept)))
         _call = mod

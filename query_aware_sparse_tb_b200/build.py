@@ -17,6 +17,8 @@ import subprocess
 import sys
 import warnings
 
+from ._lib import call_tag
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -68,9 +70,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_call(force: bool = False) -> str:
-    """_tbcall.so: a CPython module over torch's C++ headers."""
-    src = os.path.join(CSRC, "tbcall.cpp")
-    if force or not _newer(CALL, [src, os.path.join(ROOT, "include", "tb.h")]):
+    """_tbcall.so: a CPython module over torch's C++ headers, built again when
+    its sources, torch or Python are others than it was built for."""
+    src, stamp = os.path.join(CSRC, "tbcall.cpp"), os.path.join(BUILD, "_tbcall.tag")
+    tag, built = call_tag(), None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            built = f.read()
+    if force or built != tag or not _newer(CALL, [src, os.path.join(ROOT, "include", "tb.h")]):
         import sysconfig
 
         import torch
@@ -78,7 +85,7 @@ def build_call(force: bool = False) -> str:
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
         tmp = f"{CALL}.{os.getpid()}.tmp"
         cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f'-DTB_BUILT_FOR="{tag}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                "-isystem", os.path.join(base, "include"),
                "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
                "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
@@ -93,6 +100,9 @@ def build_call(force: bool = False) -> str:
                 os.remove(CALL)
             raise
         os.replace(tmp, CALL)
+        os.makedirs(BUILD, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(tag)
     return CALL
 
 

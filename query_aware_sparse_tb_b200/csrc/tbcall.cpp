@@ -262,4 +262,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tbcall", "marshalling of the mult
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tbcall() { return PyModule_Create(&module); }
+// built_for: the torch and the Python this was compiled against, which the
+// binding compares with those it runs on.
+PyMODINIT_FUNC PyInit__tbcall() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", TB_BUILT_FOR) != 0) {
+        Py_DECREF(m);
+        m = nullptr;
+    }
+    return m;
+}

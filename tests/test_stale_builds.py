@@ -3,9 +3,11 @@ message that says what to do."""
 import os
 import shutil
 import subprocess
+import types
 
 import pytest
 
+import query_aware_sparse_tb_b200 as package
 from query_aware_sparse_tb_b200 import _lib, build
 
 
@@ -44,10 +46,23 @@ def compiler(tmp_path, monkeypatch):
     return lambda: len(runs.read_text().splitlines()) if runs.exists() else 0
 
 
+def test_the_call_module_is_built_again_for_another_torch(compiler, monkeypatch):
+    build.build_call()
+    build.build_call()
+    assert compiler() == 1                        # nothing changed
+    monkeypatch.setattr(build, "call_tag", lambda: "torch 1.0, cpython-39")
+    build.build_call()
+    build.build_call()
+    assert compiler() == 2
+    os.utime(build.CALL, (0, 0))                  # older than its sources
+    build.build_call()
+    assert compiler() == 3
+
+
 def test_the_library_is_built_without_a_cpp_compiler(compiler, monkeypatch):
     build.build_call()
     monkeypatch.setattr(build, "CXX", "/no/such/compiler")
-    os.utime(build.CALL, (0, 0))                  # older than its sources
+    monkeypatch.setattr(build, "call_tag", lambda: "torch 1.0, cpython-39")
     with pytest.raises(OSError):
         build.build_call()
     assert not os.path.exists(build.CALL)         # the stale one is gone
@@ -56,3 +71,13 @@ def test_the_library_is_built_without_a_cpp_compiler(compiler, monkeypatch):
     open(build.LIB, "w").close()
     with pytest.warns(UserWarning, match="libtb.so is built, _tbcall.so is not"):
         assert build.build() == build.LIB
+
+
+def test_a_call_module_of_another_torch_is_refused(monkeypatch):
+    build.build()
+    monkeypatch.setattr(_lib, "_call", None)
+    for fake in (types.SimpleNamespace(built_for="torch 1.0, cpython-39"), types.SimpleNamespace()):
+        monkeypatch.setattr(package, "_tbcall", fake, raising=False)
+        with pytest.raises(_lib.TbError, match="built for .*rebuild"):
+            _lib._tbcall()
+        assert _lib._call is None
