@@ -10,6 +10,7 @@ import torch
 import query_aware_sparse_tb_b200 as tb
 import test_gpu_multi as multi
 from multi_dealing import Dealing
+from query_aware_sparse_tb_b200 import _lib
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -21,12 +22,11 @@ def fill_shared_memory():
     return a @ a
 
 
-def run(n, T, hkv, G, d, tree, cap=None, seed=0, repeats=1, before=None, K=None, V=None):
+def run(n, T, hkv, G, d, tree, cap=None, seed=0, repeats=1, before=None, flags=0):
     hq = hkv * G
     g = torch.Generator(device=DEV).manual_seed(seed)
     cap = cap or (max(T) + 127) // 128 * 128
-    if K is None:
-        K, V = multi.make_cache(g, len(n), hkv, cap, d, T)
+    K, V = multi.make_cache(g, len(n), hkv, cap, d, T)
     total = sum(n)
     Q = torch.randn(total + 2, hq, d, generator=g, device=DEV).to(torch.bfloat16)
     dm, mx = tb.dims(len(n), hq, hkv, d, 16, cap), max(n)
@@ -50,7 +50,7 @@ def run(n, T, hkv, G, d, tree, cap=None, seed=0, repeats=1, before=None, K=None,
             tb.tree_attn(dm, Q, K, V, qb, mx, ctx, mask, scale, out, ws)
         else:
             tb.prompt_attn(dm, Q, K, V, qb, mx, ctx, scale, out, ws)
-        assert tb.workspace_check(ws) == 0
+        assert tb.workspace_check(ws) == flags
         assert (out[total:] == 7).all()
         outs.append(out[:total])
     assert all(torch.equal(o, outs[0]) for o in outs)
@@ -132,3 +132,80 @@ def test_decode_attention_takes_turns_on_the_workspace():
     for k in (0, 2, 1, 2, 2, 0, 1, 2):
         assert torch.equal(calls[k](shared), want[k]), calls[k].__name__
     assert tb.workspace_check(shared) == 0
+
+
+def ragged(sizes, B, lo, hi, seed):
+    r = np.random.RandomState(seed)
+    n = [int(x) for x in r.choice(sizes, B)]
+    return n, [k + int(x) for k, x in zip(n, r.randint(lo, hi, B))]
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("n,T,hkv,d,cap", [
+    (*ragged([0, 1, 3, 26, 33, 60, 70], 40, 2000, 8000, 7), 8, 64, 8192),   # 312 items, sequences without tokens among them
+    (*ragged([100], 16, 12000, 16000, 8), 8, 128, 16384),                   # 256 items
+    (*ragged([1, 26, 60, 64], 32, 4000, 15000, 9), 8, 64, 16384),
+])
+def test_shares_with_more_items_than_ctas(n, T, hkv, d, cap, tree):
+    """The join entries are the CTAs', not the items'."""
+    assert not Dealing(n, T, hkv, 4, tree, n_tokens=sum(n) + 2).check().by_item
+    run(n, T, hkv, 4, d, tree, cap=cap, seed=5, repeats=2)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("hkv,d", [(1, 64), (1, 128), (4, 64)])
+def test_shares_of_more_sequences_than_a_warp_looks_at_once(hkv, d, tree):
+    """70 sequences: the line, its search and the report go on past 32; with one
+    KV head the join entries are the items', with four the CTAs'."""
+    n, T = ragged([0, 1, 3, 26, 33, 60], 70, 0, 8000, 7)
+    assert Dealing(n, T, hkv, 4, tree, n_tokens=sum(n) + 2).check().by_item == (hkv == 1)
+    run(n, T, hkv, 4, d, tree, cap=8192, seed=6, repeats=2)
+
+
+@pytest.mark.parametrize("hkv", [1, 4])
+def test_shares_with_tokens_that_have_no_row(hkv):
+    """Sequences longer than their lengths among 40, in the second 32 too: their
+    first tokens, whole items of them, see nothing and give 0."""
+    n, T = ragged([0, 1, 26, 60], 40, 100, 8000, 11)
+    for b, (k, t) in {3: (200, 100), 20: (30, 4), 35: (140, 9), 39: (65, 64)}.items():
+        n[b], T[b] = k, t
+    dealing = Dealing(n, T, hkv, 4, False, n_tokens=sum(n) + 2).check()
+    assert any(tiles == 0 for _, _, _, tiles, _, _ in dealing.line) and dealing.by_item == (hkv == 1)
+    run(n, T, hkv, 4, 64, False, cap=8192, seed=8, flags=_lib.TB_FLAG_CTX_RANGE)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_that_are_not_finite_where_the_first_slot_has_no_tile(d):
+    """The list of V rows taken out is written while a slot without tiles ends."""
+    n, T, hkv = [200], [3225], 32
+    assert Dealing(n, T, hkv, 1, False).slot0_without_tiles() > 0
+    g = torch.Generator(device=DEV).manual_seed(13)
+    K, V = multi.make_cache(g, 1, hkv, 12288, d, T)
+    clean = V.clone()
+    for row, value in ((T[0] - 1, float("nan")), (T[0] - 40, float("inf")), (T[0] - 190, float("nan"))):
+        V[:, :, row, 7], clean[:, :, row, 7] = value, 0
+    Q = torch.randn(200, hkv, d, generator=g, device=DEV).to(torch.bfloat16)
+    dm, scale = tb.dims(1, hkv, hkv, d, 16, 12288), 1 / math.sqrt(d)
+    ws = tb.workspace(tb.prompt_attn_workspace_bytes(dm, 200, 200))
+    assert ws.numel() > 1 << 20
+    ref, tol = multi.reference(Q, K, clean, n, T, scale, multi.causal(n, T))
+    keep = [c for c in range(d) if c != 7]
+    for _ in range(3):
+        fill_shared_memory()
+        out = torch.zeros_like(Q)
+        tb.prompt_attn(dm, Q, K, V, multi.i32([0, 200]), 200, multi.i32(T), scale, out, ws)
+        assert tb.workspace_check(ws) == 0
+        assert out[10:, :, 7].isnan().all()                # tokens from the first NaN's row on
+        multi.check(out[:10], ref[:10], tol[:10], "tokens before")
+        multi.check(out[10:, :, keep], ref[10:, :, keep], tol[10:, :, keep], "other values")
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_short_sequences_in_a_large_cache(tree):
+    """The rule goes by the capacity: sequences of one to three tiles are shared
+    out too, to few CTAs."""
+    n, _ = ragged(range(1, 301), 16, 0, 1, 3)
+    T = [k + (j % 3) * 10 for j, k in enumerate(n)]
+    dealing = Dealing(n, T, 2, 4, tree, n_tokens=sum(n) + 2).check()
+    assert dealing.shares < 148
+    run(n, T, 2, 4, 64, tree, cap=65536, seed=9, repeats=2)
