@@ -28,7 +28,7 @@ CALL = os.path.join(PKG, "_tbcall.so")
 SOURCES = ["api.cu", "attn.cu", "select.cu", "select_cluster.cu", "gemm_tc.cu", "noalloc.cu", "kv.cu",
            "multi_attn.cu", "rope.cu", "tree.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
-CXX = os.environ.get("CXX", "g++")
+CXX = "g++"  # the system's, whose C++ runtime torch shares: exceptions cross between the two
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-cudart", "shared", "-I", os.path.join(ROOT, "include")]
 

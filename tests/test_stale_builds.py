@@ -81,3 +81,14 @@ def test_a_call_module_of_another_torch_is_refused(monkeypatch):
         with pytest.raises(_lib.TbError, match="built for .*rebuild"):
             _lib._tbcall()
         assert _lib._call is None
+
+
+def test_the_call_module_shares_the_cpp_runtime_of_torch(monkeypatch):
+    """With a C++ runtime of its own (as a compiler that links it statically
+    gives) the module's error messages crashed the process."""
+    if shutil.which("readelf") is None:
+        pytest.skip("readelf not available")
+    monkeypatch.setenv("CXX", "/no/such/compiler")  # not the environment's choice
+    build.build_call(force=True)
+    needed = subprocess.run(["readelf", "-d", build.CALL], check=True, capture_output=True, text=True).stdout
+    assert "libstdc++.so.6" in needed
