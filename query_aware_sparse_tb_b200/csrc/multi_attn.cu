@@ -79,14 +79,6 @@ constexpr uint32_t kTmemCols = 512;
 // exponents; the sums (weights x 2^22 rows x |v|) stay finite to |v| of 2^72.
 // At 8 an 8K prompt with 1% of its keys scaled by 4 took 540 us, at 32 505.
 constexpr float kLazy = 32.0f;
-// From this |m| on the reference's logit is taken off before the product with
-// c.  m = c s_ref is rounded, so the fused c s - m of the reference itself is
-// that rounding error instead of 0: up to here the same factor in all of a
-// row's weights (below 2), but 2^64 at 2^30, and past 2^31 the weights of whole
-// rows were 0 or infinite.  The branch is that of the raise, taken in every
-// tile then: with one of its own an 8K prompt took 519 us, with this 507 (of
-// the 503 without).
-constexpr float kBig = 16777216.0f;
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 // Masked tiles of an item: its new tokens' rows (1024 at most for a tree, 256
@@ -151,6 +143,21 @@ __device__ __forceinline__ bool elect_one() {
 // wait_role by a whole warp: one answer for all lanes.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t *flags) {
     return __all_sync(kFullMask, wait_role(bar, parity, abort_flag, flags));
+}
+
+// What a row's c and m are multiplied by for its weights 2^(s c - m): 1, and from
+// |m| = 2^30 on the power of two that brings m below that.  m is a rounded
+// product s_ref c and the fused s c - m keeps its rounding error as a common
+// factor of the row's weights: no error, but 2^64 for |m| at 2^30, and past
+// 2^31 the weights of whole rows were 0 or infinite.  Scaled, the factor stays
+// within 2^32, and no weight that counts changes: logits that differ do so by
+// 2^5 or more as scaled, by a multiple of that in truth, so all but the ones
+// equal to the largest have weights below 2^-32 either way.  (To take s_ref off
+// each logit first is 64 to 128 instructions more beside the path of the raise:
+// a tree over 64K 59.0 -> 60.5 to 61.7 us; with the factor 59.3.)
+__device__ __forceinline__ float row_factor(float m) {
+    const int e = (__float_as_int(m) >> 23) & 0xff;
+    return m == -INFINITY ? 1.f : __int_as_float((127 - max(0, e - (127 + 29))) << 23);
 }
 
 // bits 0 .. n-1 set (n clamped to [0, 32])
@@ -1041,8 +1048,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 masked_from = p.mask ? base : base + f[kTok0] + (pair ? slot * tps : 0) + 1;
             }
             float m = -INFINITY, l = 0.f;
-            float ref = 0.f;   // the logit that m is the product of
-            bool big = false;  // some row of the warp is at or past kBig
+            float rf = 1.f;  // row_factor(m)
             // a warp whose 32 rows all lie behind the item's last token only
             // keeps the barriers going: its rows' weights and sums are whatever
             // the columns hold, and nobody reads them
@@ -1118,8 +1124,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         mx[q] = max3_nan(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx[q] = max3_nan(mx[q], __uint_as_float(s[q][31]), mx[q]);
-                const float top_s = max3_nan(mx[0], mx[1], max3_nan(mx[2], mx[3], mx[3]));
-                float top = top_s * p.c;
+                float top = max3_nan(mx[0], mx[1], max3_nan(mx[2], mx[3], mx[3])) * p.c;
                 // a NaN or +inf logit makes the row's softmax NaN: so becomes m, and l with it
                 if (!(top < INFINITY)) top = NAN;
                 const bool raise = !(top <= m + kLazy);  // also the first logit of a row (m = -inf)
@@ -1128,7 +1133,7 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (!ok) break;
                     tc_fence_after();
                 }
-                if (__any_sync(kFullMask, raise || big)) {
+                if (__any_sync(kFullMask, raise)) {
                     const float m_new = raise ? top : m;
                     const float fac = m_new == m ? 1.f : ex2(m - m_new);  // (-inf stays -inf while nothing is seen)
                     if (j > 0) {
@@ -1147,18 +1152,10 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                     l *= fac;
                     m = m_new;
-                    if (raise) ref = top_s;
-                    big = __any_sync(kFullMask, fabsf(m) >= kBig && m != -INFINITY);
-                    if (big) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) s[q][i] = __float_as_uint(__uint_as_float(s[q][i]) - ref);
-                    }
+                    rf = row_factor(m);
                 }
-                // (a row that has seen nothing: 2^(-inf - 0) = 0)
-                const float mm = m == -INFINITY || big ? 0.f : m;
-                const uint64_t c2 = pack2(p.c, p.c), nm2 = pack2(-mm, -mm);
+                const float mm = m == -INFINITY ? 0.f : m * rf;  // a row that has seen nothing: 2^(-inf - 0) = 0
+                const uint64_t c2 = pack2(p.c * rf, p.c * rf), nm2 = pack2(-mm, -mm);
                 uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -1280,7 +1277,8 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll 1
                         for (int i = 0; i < D; ++i)
                             x = fmaf(__uint_as_float((uint32_t)qr[i] << 16), __uint_as_float((uint32_t)p.K[kv + i] << 16), x);
-                        x = ex2(__fadd_rn(__fmul_rn(x, p.c), -m)) * (part_slot < 0 ? 1.f / l : 1.f);
+                        rf = row_factor(m);
+                        x = ex2(fmaf(x, p.c * rf, -m * rf)) * (part_slot < 0 ? 1.f / l : 1.f);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             o[i] = fmaf(x, __uint_as_float((uint32_t)p.V[kv + q * 16 + i] << 16), o[i]);

@@ -22,7 +22,7 @@ DEV = "cuda"
 @pytest.mark.parametrize("shares", [False, True])
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("power", [17, 24, 28, 31, 33, 40, 60, 100])
+@pytest.mark.parametrize("power", [17, 24, 28, 29, 30, 31, 32, 33, 40, 60, 100, 120])
 def test_large_logits(power, d, tree, shares):
     n, T, hq, hkv = [70, 20], [900, 20], 8, 2
     cap = 16384 if shares else 1024
