@@ -44,14 +44,16 @@
 //   - long prompts: the tensor cores and the power they draw.  A tile of 256
 //     rows x 128 keys is 2,048 cycles of products and takes about 3,100, the
 //     rest being the latency of the chain S, softmax, PV within a slot; 32K
-//     tokens run 6.7 ms from a cold GPU (1,310 TFLOP/s) and 7.5 ms once the
-//     power cap holds the clock near 1.55 GHz (1,165 TFLOP/s; a plain bf16
+//     tokens run 6.7 ms from a cold GPU (1,310 TFLOP/s) and 7.6 to 7.7 ms once
+//     the power cap holds the clock near 1.55 GHz (1,145 TFLOP/s; a plain bf16
 //     matrix product does 1,400 there).
-//   - 64 head dims: the softmax (the products are half as long, the
-//     exponentials as many): 735 TFLOP/s at 8K tokens.
-//   - trees and decode steps over long contexts: HBM.  26 drafted tokens over
-//     64K rows take 58 us in a graph.  37 of them stream 269 MB; the rest is
-//     the launches, the start (5 us), the states (3 us) and their join (5 us).
+//   - 64 head dims: the waits between softmax and products.  The products are
+//     half as long, the exponentials as many; the exponential unit is 70 % busy
+//     and the tensor cores 35 %: 730 TFLOP/s for ragged prompts of 0.5K to 5K.
+//   - trees and single tokens over long contexts: HBM first.  26 drafted tokens
+//     over 64K rows (269 MB, 41 us at the copy rate) take 59 to 60 us back to
+//     back.  Without the join it is 6 less; the rest is the start of the work,
+//     its ragged end and the writing of 10 MB of states.
 #include <cuda.h>
 #include <math.h>
 
@@ -1167,15 +1169,18 @@ multi_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         // (a quarter of the exponentials by a polynomial on
                         // the FMA pipe, beside the unit's 16 a cycle, made no
                         // difference under the power cap: 510 against 512 us
-                        // for an 8K prompt)
+                        // for an 8K prompt of 128 head dims; not measured at 64)
                         float e0, e1;
                         unpack2(x2, e0, e1);
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
                         // rounded to bf16 for the second product: at most 2^-8
-                        // relative per weight, as the rounding of the result,
-                        // and of either sign, so a row's errors mostly cancel
+                        // relative per weight, as the rounding of the result.
+                        // Together they are off by 0.0023 (2-norm), the result
+                        // alone by 0.0017; a product with the remainders too
+                        // would be half as much tensor work again, which is
+                        // what bounds the prompts
                         w[i] = pack_bf16(e0, e1);
                     }
                     tmem_st16(tp + q * 16, w);
@@ -1462,7 +1467,10 @@ long long item_bound(const tb_dims &d, int32_t n_tokens, int32_t max_new) {
 // that may come last; at least one whole item.  Shares are even but write and
 // join states, about 16 tiles' time
 // (992 items of 25 to 64 tiles: 371 us in shares, 358 by the counter; 16 items of
-// 514 tiles: 141 against 838).
+// 514 tiles: 141 against 838).  Where the cache is much larger than what it
+// holds the rule takes short sequences for long ones: 16 prompts of 1 to 300
+// tokens 11.6 us in a cache of 512 rows, by the counter, and 22.4 in one of
+// 64K, in shares; five of 500 to 5,000 tokens 347 us (8K rows) and 362 (64K).
 bool use_shares(const tb_dims &d, int32_t max_new, bool tree, long long items) {
     const double ctas = num_sms(), n = (double)items * d.n_kv_heads;
     const double longest = (d.ctx_cap + kTile - 1) / kTile;

@@ -19,8 +19,11 @@
 // the norm one reduction over the lanes.  A lane keeps the 4 (cos, sin) pairs
 // of its values in registers for all of the token's heads.
 //
-// On a B200, 32 query and 8 KV heads of 128: 32K tokens (805 MB moved) 127 us
-// in a graph, 6.34 TB/s or 0.97 of a plain copy; 16 tokens 3.1 us, the launch.
+// On a B200, 32 query and 8 KV heads of 128: 32K tokens (805 MB moved) 126 us
+// in a graph, 6.4 TB/s or 0.97 of a plain copy, and 134 to 138 in a loop of
+// calls (0.90); 16 tokens 3.1 us, the launch.  24 heads of 64: 13.2 us for 8.4K
+// tokens (52 MB), 22.2 for 16.9K, 40.9 for 33.8K, that is 3.5 us and 5.5 TB/s,
+// whether of one sequence or eight and with 4 or 16 of the pairs turned.
 #include "common.cuh"
 #include "internal.h"
 #include "multi.h"
