@@ -1,5 +1,7 @@
 """Calls for several new tokens that the documentation allows and that are easy
 to get wrong."""
+import math
+
 import pytest
 import torch
 
@@ -67,3 +69,70 @@ def test_accept_moves_a_cache_that_is_listed_twice_once(caches_of):
         kv, want, new_len, flags = accept_case([13, 21], n, T, path, caches_of)
         assert flags == 0 and new_len == [37, 45]
         assert torch.equal(kv, want)
+
+
+# ------------------------------------------------------------------ into the decode path
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_prompt_leads_into_the_sparse_decode_step(d):
+    """A prompt fills the cache, its keys are projected, the next token is
+    scored, selects and attends: captured without a wait between the calls and
+    replayed over cleared caches, the same bits as with a wait after each call.
+    With a budget of the whole context the step is dense attention."""
+    hq, hkv, dp, cap, n, T = 8, 2, 16, 640, [300, 41], [300, 41]
+    sink, window, nbr = 4, 8, 1
+    dm, total, scale = tb.dims(2, hq, hkv, d, dp, cap), sum(n), 1 / math.sqrt(d)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    qkv, step_qkv = rnd(total, (hq + 2 * hkv) * d), rnd(2, (hq + 2 * hkv) * d)
+    Wk, qp = rnd(hkv, dp, d), torch.randn(2, hq, dp, generator=g, device=DEV)
+    inv = 10000.0 ** (-2 * torch.arange(d // 2, dtype=torch.float64, device=DEV) / d)
+    qb, one, ctx, ctx1 = i32(multi.starts(n)), i32([0, 1, 2]), i32(T), i32([t + 1 for t in T])
+    begin, count = i32([0, 0]), i32([t + 1 for t in T])
+
+    def buffers(budget):
+        z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device=DEV)  # noqa: E731
+        return dict(K=z(2, hkv, cap, d), V=z(2, hkv, cap, d), Kp=z(2, hkv, cap, dp), Q=z(total, hq, d), Q1=z(2, hq, d),
+                    out=z(total, hq, d), out1=z(2, hq, d, t=torch.float32), budget=budget,
+                    idx=z(2, hq, min(3 * budget, cap), t=torch.int32), cnt=z(2, hq, t=torch.int32),
+                    bits=z(2, hq, cap // 32, t=torch.int32), ws=tb.workspace(256),
+                    wp=tb.workspace(tb.prompt_attn_workspace_bytes(dm, total, 300)),
+                    wsel=tb.workspace(tb.score_select_workspace_bytes(dm)), wa=tb.workspace(tb.attn_workspace_bytes(dm)))
+
+    def chain(y, after=lambda: None):
+        rope = lambda x, q, c, Q: tb.norm_rope_append(dm, x, q, c, None, None, None, 0.0, inv, False, Q, y["K"], y["V"], y["ws"])  # noqa: E731
+        for call in (
+            lambda: rope(qkv, qb, ctx, y["Q"]),
+            lambda: tb.prompt_attn(dm, y["Q"], y["K"], y["V"], qb, 300, ctx, scale, y["out"], y["wp"]),
+            lambda: rope(step_qkv, one, ctx1, y["Q1"]),
+            lambda: tb.project_keys(dm, y["K"], Wk, y["Kp"], begin, count, 301, y["ws"]),
+            lambda: tb.score_select(dm, qp, hq * dp, y["Kp"], ctx1, sink, window, y["budget"], nbr, y["idx"], y["cnt"],
+                                    y["bits"], y["wsel"]),
+            lambda: tb.sparse_decode_attn(dm, y["Q1"], y["K"], y["V"], ctx1, sink, window, y["bits"], scale, y["out1"],
+                                          y["wa"]),
+        ):
+            call()
+            after()
+
+    for budget in (16, cap):
+        want, got = buffers(budget), buffers(budget)
+        chain(want, torch.cuda.synchronize)
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                chain(got)
+        torch.cuda.current_stream().wait_stream(side)
+        for _ in range(3):
+            for name in ("K", "V", "Kp", "Q", "Q1", "out", "out1", "bits"):
+                got[name].zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for name in ("K", "V", "Kp", "Q", "Q1", "out", "out1", "bits", "cnt"):
+                assert torch.equal(got[name], want[name]), (budget, name)
+        for name in ("ws", "wp", "wsel", "wa"):
+            assert tb.workspace_check(got[name]) == 0 and tb.workspace_check(want[name]) == 0
+        multi.check(want["out"], *multi.reference(want["Q"], want["K"], want["V"], n, T, scale, multi.causal(n, T)), "prompt")
+    T1 = [t + 1 for t in T]
+    multi.check(want["out1"], *multi.reference(want["Q1"], want["K"], want["V"], [1, 1], T1, scale, multi.causal([1, 1], T1)),
+                "decode step")
