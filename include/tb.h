@@ -59,6 +59,8 @@
 extern "C" {
 #endif
 
+/* Raised when an existing entry point or structure changes; entry points may be
+ * added within a version. */
 #define TB_ABI_VERSION 10
 
 typedef uint16_t tb_bf16;

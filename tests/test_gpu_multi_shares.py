@@ -209,3 +209,77 @@ def test_short_sequences_in_a_large_cache(tree):
     dealing = Dealing(n, T, 2, 4, tree, n_tokens=sum(n) + 2).check()
     assert dealing.shares < 148
     run(n, T, 2, 4, 64, tree, cap=65536, seed=9, repeats=2)
+
+
+@pytest.mark.parametrize("cap", [1152, 32768])        # whole items; shares
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 16)])
+def test_the_largest_tree_with_odd_rows_in_every_tile(d, G, cap):
+    """1,024 drafted tokens that begin and end inside a tile: nine tiles with
+    values that are not finite, each seen by its own token and one other."""
+    n, T, hkv = [1024], [1061], 2
+    g = torch.Generator(device=DEV).manual_seed(d)
+    K, V = multi.make_cache(g, 1, hkv, cap, d, T)
+    clean = V.clone()
+    r = np.random.RandomState(d)
+    mask = r.rand(1024, 1024) < 0.02
+    odd = list(range(3, 1024, 120))
+    mask[:, odd] = False
+    seen = set()
+    for k, j in enumerate(odd):
+        other = (j * 7 + 500) % 1024
+        mask[j, j] = mask[other, j] = True
+        seen |= {j, other}
+        V[:, :, 37 + j, 7], clean[:, :, 37 + j, 7] = float("nan") if k % 2 else float("inf"), 0
+    Q = torch.randn(1024, hkv * G, d, generator=g, device=DEV).to(torch.bfloat16)
+    out, dm, scale = torch.zeros_like(Q), tb.dims(1, hkv * G, hkv, d, 16, cap), 1 / math.sqrt(d)
+    ws = tb.workspace(tb.tree_attn_workspace_bytes(dm, 1024, 1024))
+    assert (ws.numel() > 256) == (cap > 2000)
+    tb.tree_attn(dm, Q, K, V, multi.i32([0, 1024]), 1024, multi.i32(T), multi.pack_rows(mask, 32), scale, out, ws)
+    assert tb.workspace_check(ws) == 0
+    ref, tol = multi.reference(Q, K, clean, n, T, scale, multi.tree_see([mask], n, T))
+    dirty = torch.zeros(1024, dtype=torch.bool, device=DEV)
+    dirty[sorted(seen)] = True
+    assert not out[dirty][:, :, 7].isfinite().any()
+    multi.check(out[~dirty], ref[~dirty], tol[~dirty], "tokens that see none")
+    keep = [c for c in range(d) if c != 7]
+    multi.check(out[:, :, keep], ref[:, :, keep], tol[:, :, keep], "other values")
+
+
+def test_calls_from_several_host_threads():
+    """Each thread its stream, workspace and outputs; the cache is shared."""
+    import threading
+    n, T, hkv, d = [40, 9], [3000, 700], 2, 128
+    g = torch.Generator(device=DEV).manual_seed(1)
+    K, V = multi.make_cache(g, 2, hkv, 4096, d, T)
+    Q = torch.randn(49, 8, d, generator=g, device=DEV).to(torch.bfloat16)
+    dm, scale, qb, ctx = tb.dims(2, 8, hkv, d, 16, 4096), 1 / math.sqrt(d), multi.i32([0, 40, 49]), multi.i32(T)
+    size = tb.prompt_attn_workspace_bytes(dm, 49, 40)
+    want = torch.zeros_like(Q)
+    tb.prompt_attn(dm, Q, K, V, qb, 40, ctx, scale, want, tb.workspace(size))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                ws = tb.workspace(size)
+                for _ in range(50):
+                    out = torch.zeros_like(Q)
+                    tb.prompt_attn(dm, Q, K, V, qb, 40, ctx, scale, out, ws)
+                    with pytest.raises(tb.TbError, match="max_new"):
+                        tb.prompt_attn(dm, Q, K, V, qb, 0, ctx, scale, out, ws)
+                    stream.synchronize()
+                    if not torch.equal(out, want):
+                        wrong.append("differs")
+                if tb.workspace_check(ws):
+                    wrong.append("flag")
+        except BaseException as e:  # noqa: BLE001
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
