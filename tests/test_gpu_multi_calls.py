@@ -136,3 +136,59 @@ def test_a_prompt_leads_into_the_sparse_decode_step(d):
     T1 = [t + 1 for t in T]
     multi.check(want["out1"], *multi.reference(want["Q1"], want["K"], want["V"], [1, 1], T1, scale, multi.causal([1, 1], T1)),
                 "decode step")
+
+
+# ------------------------------------------------------------------ nothing beside the outputs
+
+def guarded(shape, dtype, fill, pad=4096):
+    """A tensor in the middle of a buffer of a known pattern, and a check that
+    the pattern beside it is still there."""
+    nbytes = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((pad + nbytes + pad,), 0x5C, dtype=torch.uint8, device=DEV)
+    t = buf[pad:pad + nbytes].view(dtype).view(shape)
+    if fill is not None:
+        t.copy_(fill)
+    return t, lambda: bool((buf[:pad] == 0x5C).all()) and bool((buf[pad + nbytes:] == 0x5C).all())
+
+
+@pytest.mark.parametrize("cap", [513, 32768])         # whole items; shares
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_write_nothing_beside_their_outputs(d, cap):
+    n, T, hq, hkv = [33, 0, 70, 1], [400, 0, 513, 1], 8, 2
+    g = torch.Generator(device=DEV).manual_seed(d)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    dm, total = tb.dims(4, hq, hkv, d, 16, cap), sum(n)
+    qb, ctx = i32(multi.starts(n)), i32(T)
+    K, k_ok = guarded((4, hkv, cap, d), torch.bfloat16, rnd(4, hkv, cap, d))
+    V, v_ok = guarded((4, hkv, cap, d), torch.bfloat16, rnd(4, hkv, cap, d))
+    Q, q_ok = guarded((total, hq, d), torch.bfloat16, None)
+    out, o_ok = guarded((total, hq, d), torch.bfloat16, None)
+    new_len, l_ok = guarded((4,), torch.int32, None)
+    small, s_ok = guarded((256,), torch.uint8, torch.zeros(256, dtype=torch.uint8, device=DEV))
+    qkv = rnd(total, (hq + 2 * hkv) * d)
+    tb.norm_rope_append(dm, qkv, qb, ctx, None, None, None, 0.0, None, False, Q, K, V, small)
+    x = qkv.view(total, hq + 2 * hkv, d)
+    assert torch.equal(Q, x[:, :hq]) and q_ok() and k_ok() and v_ok() and s_ok()
+    K0, V0 = K.clone(), V.clone()
+    for tree in (False, True):
+        size = (tb.tree_attn_workspace_bytes if tree else tb.prompt_attn_workspace_bytes)(dm, total, 70)
+        assert (size > 256) == (cap > 1000)
+        ws, w_ok = guarded((size,), torch.uint8, torch.zeros(size, dtype=torch.uint8, device=DEV))
+        for _ in range(2):
+            if tree:
+                mask = torch.full((total, 3), -1, dtype=torch.int32, device=DEV)
+                tb.tree_attn(dm, Q, K, V, qb, 70, ctx, mask, 0.1, out, ws)
+            else:
+                tb.prompt_attn(dm, Q, K, V, qb, 70, ctx, 0.1, out, ws)
+        assert tb.workspace_check(ws) == 0 and w_ok() and o_ok() and q_ok() and k_ok() and v_ok()
+        assert torch.equal(K, K0) and torch.equal(V, V0) and torch.equal(Q, x[:, :hq])
+    caches = torch.tensor([K.data_ptr(), V.data_ptr()], dtype=torch.int64, device=DEV)
+    path = i32([list(range(1, 33)), [0] * 32, list(range(38, 70)), [0] * 32])
+    tb.tree_accept(dm, 1, caches, qb, ctx, path, i32([32, 0, 32, 1]), new_len, small)
+    assert tb.workspace_check(small) == 0 and new_len.tolist() == [399, 0, 475, 1]
+    for now, was in ((K, K0), (V, V0)):
+        want = was.clone()
+        want[0, :, 367:399] = was[0, :, 368:400]
+        want[2, :, 443:475] = was[2, :, 481:513]
+        assert torch.equal(now, want)
+    assert k_ok() and v_ok() and l_ok() and s_ok()
